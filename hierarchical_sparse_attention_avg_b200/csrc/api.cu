@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "dense.cuh"
 #include "internal.h"
 
 namespace lh {
@@ -231,6 +232,25 @@ int make_tmap_f16_4d(CUtensorMap* map, const void* base, int d, int rows, int bh
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? LH_OK : LH_ERR_CUDA;
 }
+
+int make_tmap_dense(CUtensorMap* map, const DenseTensor& t, int d, int S, int H, int B, int pack, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return LH_ERR_CUDA;
+  const cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)pack, (cuuint64_t)S, (cuuint64_t)(H / pack), (cuuint64_t)B};
+  // a dimension of one is never stepped over: any valid stride stands for it
+  const int64_t es[4] = {t.st.h, t.st.s, t.st.h * pack, t.st.b};
+  cuuint64_t strides[4];
+  for (int i = 0; i < 4; ++i) strides[i] = dims[i + 1] == 1 ? (cuuint64_t)d * 2 : (cuuint64_t)es[i] * 2;
+  const cuuint32_t box[5] = {64, (cuuint32_t)pack, (cuuint32_t)box_rows, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void*>(t.p), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LH_OK : LH_ERR_CUDA;
+}
+
+// Device status word of the current device, for the other translation units.
+int device_status(int** out) { return status_ptr(out); }
 
 }  // namespace lh
 

@@ -1,0 +1,158 @@
+// dense_api.cu — the C ABI of the dense stage's attention (lh_attn_*): validation, sizes, workspace layout and the
+// launch sequences.  Semantics are documented in include/lh.h.
+#include <math.h>
+#include <string.h>
+
+#include "dense.cuh"
+
+namespace lh {
+namespace {
+
+constexpr size_t kAlign = 256;
+inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+inline bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
+inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+int validate(const lh_attn_params* P) {
+  if (!P) return LH_ERR_INVALID_ARG;
+  if (P->B < 1 || P->Hq < 1 || P->Hkv < 1 || P->Sq < 1 || P->Skv < 1 || P->d < 1 || P->Hq % P->Hkv)
+    return LH_ERR_INVALID_ARG;
+  if ((P->dtype != LH_BF16 && P->dtype != LH_FP16) || (P->causal & ~1) || (P->bidirectional & ~1))
+    return LH_ERR_INVALID_ARG;
+  if (!(P->scale > 0.f) || !(P->softcap >= 0.f) || isinf(P->scale) || isinf(P->softcap)) return LH_ERR_INVALID_ARG;
+  if (P->buckets) {
+    if (P->buckets < 2 || P->buckets > LH_MAX_BUCKETS) return LH_ERR_INVALID_ARG;
+    if (P->bidirectional && (P->buckets < 4 || P->buckets % 2)) return LH_ERR_INVALID_ARG;
+    const int n = P->bidirectional ? P->buckets / 2 : P->buckets;
+    if (P->max_distance <= n / 2) return LH_ERR_INVALID_ARG;
+  }
+  if (P->d != 64 && P->d != 128) return LH_ERR_UNSUPPORTED;
+  if ((int64_t)P->B * P->Hq > 65535 || P->Skv > kMaxDenseKeys) return LH_ERR_UNSUPPORTED;
+  if ((int64_t)P->B * P->Hq * P->Sq > INT32_MAX) return LH_ERR_UNSUPPORTED;
+  return LH_OK;
+}
+
+// First sizes of the buckets.  The border of bucket b is e (D / e)^((b - e) / (n - e)); in 64-bit mantissas its error is
+// far below the distance of a border that is not whole from the next whole number, so one within 1e-15 of a whole
+// number is that number.
+void bucket_starts(const lh_attn_params& P, BucketStarts* s) {
+  memset(s, 0, sizeof(*s));
+  if (!P.buckets) return;
+  s->both = P.bidirectional;
+  s->n = P.bidirectional ? P.buckets / 2 : P.buckets;
+  const int e = s->n / 2;
+  for (int b = 0; b < s->n; ++b) {
+    if (b < e) { s->start[b] = b; continue; }
+    const long double x = e * powl((long double)P.max_distance / e, (long double)(b - e) / (s->n - e));
+    const long double near = roundl(x);
+    s->start[b] = (int)(fabsl(x - near) <= 1e-15L * x ? near : ceill(x));
+  }
+}
+
+int make_dense(const lh_attn_params* P, const lh_attn_mods* M, DenseDims* a, BucketStarts* bs) {
+  const int rc = validate(P);
+  if (rc) return rc;
+  static const lh_attn_mods none = {};
+  if (!M) M = &none;
+  memset(a, 0, sizeof(*a));
+  a->B = P->B; a->Hq = P->Hq; a->Hkv = P->Hkv; a->G = P->Hq / P->Hkv; a->Sq = P->Sq; a->Skv = P->Skv; a->d = P->d;
+  a->f16 = P->dtype == LH_FP16;
+  a->causal = P->causal;
+  a->scale = P->scale;
+  a->cap = P->softcap;
+  if ((P->buckets > 0) != (M->table != nullptr) || (M->slopes && M->table)) return LH_ERR_INVALID_ARG;
+  if (M->prefix && !P->causal) return LH_ERR_INVALID_ARG;
+  if (!aligned4(M->slopes) || !aligned4(M->docs) || !aligned4(M->prefix) || !aligned4(M->kv_len) ||
+      ((uintptr_t)M->table & 1u))
+    return LH_ERR_INVALID_ARG;
+  a->buckets = P->buckets;
+  a->slopes = M->slopes; a->table = M->table; a->docs = M->docs; a->prefix = M->prefix; a->kv_len = M->kv_len;
+  bucket_starts(*P, bs);
+  if (P->buckets) {  // beyond the last bucket's first size, and beyond the longest distance, nothing changes
+    a->near = bs->start[bs->n - 1];
+    if (a->near > P->Skv) a->near = P->Skv;
+  }
+  return device_status(&a->status);
+}
+
+// Checks a tensor and takes its strides (a dimension of one gets those of a contiguous tensor).
+bool take(const lh_tensor* t, int B, int H, int S, int d, DenseTensor* out) {
+  if (!t || !aligned16(t->ptr)) return false;
+  const int64_t lim = int64_t(1) << 38;  // the tensor map's strides are below 2^40 bytes
+  const int64_t st[3] = {B > 1 ? t->stride_b : (int64_t)d, H > 1 ? t->stride_h : (int64_t)d, S > 1 ? t->stride_s : (int64_t)d};
+  for (int64_t v : st)
+    if (v <= 0 || v % 8 || v > lim) return false;
+  out->p = t->ptr;
+  out->st = Strides{st[0], st[1], st[2]};
+  return true;
+}
+
+struct DenseWs {
+  size_t kdoc, part_o, part_lse, fwd_total;
+};
+DenseWs dense_ws(const DenseDims& a) {
+  DenseWs w;
+  const size_t nk = (a.Skv + kKeyTile - 1) / kKeyTile;
+  const DenseFwdPlan f = dense_fwd_plan(a);
+  const size_t rows = f.nsplit > 1 ? (size_t)f.nsplit * a.B * a.Hq * a.Sq : 0;
+  size_t o = 0;
+  w.kdoc = o; o = align_up(o + (size_t)a.B * nk * sizeof(int2));
+  w.part_o = o; o = align_up(o + rows * a.d * 4);
+  w.part_lse = o; o = align_up(o + rows * 4);
+  w.fwd_total = o;
+  return w;
+}
+
+}  // namespace
+}  // namespace lh
+
+using namespace lh;
+
+#define LH_TRY(expr)        \
+  do {                      \
+    const int rc_ = (expr); \
+    if (rc_) return rc_;    \
+  } while (0)
+
+extern "C" {
+
+int lh_attn_validate(const lh_attn_params* P) { return validate(P); }
+
+size_t lh_attn_workspace_bytes(const lh_attn_params* P, int backward) {
+  if (validate(P)) return 0;
+  DenseDims a;
+  memset(&a, 0, sizeof(a));
+  a.B = P->B; a.Hq = P->Hq; a.Hkv = P->Hkv; a.G = P->Hq / P->Hkv; a.Sq = P->Sq; a.Skv = P->Skv; a.d = P->d;
+  a.buckets = P->buckets;
+  const DenseWs w = dense_ws(a);
+  return w.fwd_total;
+}
+
+int lh_attn_bucket_starts(const lh_attn_params* P, int32_t* starts) {
+  if (validate(P) || !P->buckets || !starts) return -1;
+  BucketStarts s;
+  bucket_starts(*P, &s);
+  memcpy(starts, s.start, s.n * sizeof(int32_t));
+  return s.n;
+}
+
+int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
+                    const lh_tensor* v, const lh_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  DenseDims a;
+  BucketStarts bs;
+  LH_TRY(make_dense(P, M, &a, &bs));
+  DenseTensor tq, tk, tv, to;
+  if (!take(q, a.B, a.Hq, a.Sq, a.d, &tq) || !take(k, a.B, a.Hkv, a.Skv, a.d, &tk) ||
+      !take(v, a.B, a.Hkv, a.Skv, a.d, &tv) || !take(o, a.B, a.Hq, a.Sq, a.d, &to) || !lse || !aligned4(lse))
+    return LH_ERR_INVALID_ARG;
+  const DenseWs w = dense_ws(a);
+  if (!aligned16(ws) || ws_bytes < w.fwd_total) return ws ? LH_ERR_WORKSPACE : LH_ERR_INVALID_ARG;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  cudaStream_t st = (cudaStream_t)stream;
+  int2* kdoc = reinterpret_cast<int2*>(wsb + w.kdoc);
+  if (a.docs) LH_TRY(launch_dense_doc_ranges(a, kdoc, nullptr, st));
+  return launch_dense_fwd(a, bs, tq, tk, tv, const_cast<void*>(to.p), to.st, lse, kdoc,
+                          reinterpret_cast<float*>(wsb + w.part_o), reinterpret_cast<float*>(wsb + w.part_lse), st);
+}
+
+}  // extern "C"

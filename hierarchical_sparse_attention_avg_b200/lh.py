@@ -38,6 +38,25 @@ class LhKernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int32), ("ms", ctypes.c_double)]
 
 
+LH_BF16 = 0
+LH_FP16 = 1
+LH_MAX_BUCKETS = 128
+
+
+class LhAttnParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "Sq", "Skv", "d", "dtype", "causal")] +
+                [(n, ctypes.c_float) for n in ("scale", "softcap")] +
+                [(n, ctypes.c_int32) for n in ("buckets", "max_distance", "bidirectional")])
+
+
+class LhTensor(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("stride_b", "stride_h", "stride_s")]
+
+
+class LhAttnMods(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("slopes", "table", "docs", "prefix", "kv_len")]
+
+
 class LighthouseError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -75,6 +94,10 @@ _SIGS = {
     "lh_step_host_bytes": (ctypes.c_size_t, [_P, ctypes.c_int]),
     "lh_step_host": (ctypes.c_int, [_P, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, ctypes.c_size_t, _vp,
                                     _vp, _vp]),
+    "lh_attn_validate": (ctypes.c_int, [_vp]),
+    "lh_attn_workspace_bytes": (ctypes.c_size_t, [_vp, ctypes.c_int]),
+    "lh_attn_bucket_starts": (ctypes.c_int, [_vp, _vp]),
+    "lh_attn_forward": (ctypes.c_int, [_vp] * 8 + [ctypes.c_size_t, _vp]),
 }
 
 
@@ -454,3 +477,137 @@ def lh_score_topk_static(P: Params, k, scores_in=None, scores_out=None, idx_g=No
                                    _ptr(slot), _stream(dev))
     _check(rc, "lh_score_topk_static")
     return idx_g, slot
+
+
+# ------------------------------------------------------------------------------------------------------------
+# Dense-stage attention (capped scores, distance biases, document and prefix masks; lengths over a cache)
+# ------------------------------------------------------------------------------------------------------------
+
+_ATTN_DTYPES = {torch.bfloat16: LH_BF16, torch.float16: LH_FP16}
+
+
+@dataclass(frozen=True)
+class AttnParams:
+    """Sizes and score function of ``lh_attn_forward`` / ``lh_attn_backward`` (see ``lh_attn_params`` in
+    ``include/lh.h``).  ``scale`` None is d**-0.5."""
+
+    B: int
+    Hq: int
+    Hkv: int
+    Sq: int
+    Skv: int
+    d: int
+    dtype: torch.dtype = torch.bfloat16
+    causal: bool = True
+    scale: float | None = None
+    softcap: float = 0.0
+    buckets: int = 0
+    max_distance: int = 0
+    bidirectional: bool = False
+
+    def __post_init__(self):
+        if self.dtype not in _ATTN_DTYPES:
+            raise ValueError(f"dtype: expected torch.bfloat16 or torch.float16, got {self.dtype}")
+        scale = (self.d ** -0.5 if self.d > 0 else 1.0) if self.scale is None else self.scale
+        c = LhAttnParams(self.B, self.Hq, self.Hkv, self.Sq, self.Skv, self.d, _ATTN_DTYPES[self.dtype],
+                         1 if self.causal else 0, scale, self.softcap, self.buckets, self.max_distance,
+                         1 if self.bidirectional else 0)
+        object.__setattr__(self, "_c", c)  # read by every call, built once
+        object.__setattr__(self, "_ref", ctypes.addressof(c))
+        object.__setattr__(self, "_status", _lib.lh_attn_validate(self._ref))
+
+    def c(self) -> LhAttnParams:
+        return self._c
+
+
+def lh_attn_validate(P: AttnParams) -> int:
+    return P._status
+
+
+def lh_attn_workspace_bytes(P: AttnParams, backward: bool = False) -> int:
+    return _lib.lh_attn_workspace_bytes(P._ref, 1 if backward else 0)
+
+
+def new_attn_workspace(P: AttnParams, device, backward: bool = False) -> torch.Tensor:
+    """Scratch for calls with ``P``; one at a time may use it (calls on one stream may share it)."""
+    _check(P._status, "lh_attn_workspace_bytes")
+    return torch.empty(lh_attn_workspace_bytes(P, backward), dtype=torch.uint8, device=device)
+
+
+def lh_attn_bucket_starts(P: AttnParams) -> list:
+    """First distance of each bucket of one direction."""
+    buf = (ctypes.c_int32 * LH_MAX_BUCKETS)()
+    n = _lib.lh_attn_bucket_starts(P._ref, buf)
+    if n < 0:
+        raise LighthouseError(LH_ERR_INVALID_ARG, "lh_attn_bucket_starts")
+    return list(buf[:n])
+
+
+def _rows(t, shape, dtype, device, name) -> LhTensor:
+    """Descriptor of a [B, H, S, d] tensor with any layout the library takes: unit feature stride, the others multiples
+    of 8 elements."""
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    sb, sh, ss, sd = t.stride()
+    B, H, S, d = shape
+    if sd != 1 or (B > 1 and (sb <= 0 or sb & 7)) or (H > 1 and (sh <= 0 or sh & 7)) or (S > 1 and (ss <= 0 or ss & 7)):
+        raise ValueError(f"{name}: features must be contiguous and the other strides positive multiples of 8, got {t.stride()}")
+    return LhTensor(t.data_ptr(), sb, sh, ss)
+
+
+def _vec(t, shape, dtype, device, name):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _attn_mods(P: AttnParams, dev, slopes, table, docs, prefix, kv_len) -> LhAttnMods:
+    return LhAttnMods(_vec(slopes, (P.Hq,), torch.float32, dev, "slopes"),
+                      _vec(table, (P.Hq, P.buckets), P.dtype, dev, "table"),
+                      _vec(docs, (P.B, P.Skv), torch.int32, dev, "docs"),
+                      _vec(prefix, (P.B,), torch.int32, dev, "prefix"),
+                      _vec(kv_len, (P.B,), torch.int32, dev, "kv_len"))
+
+
+def _attn_ws(P: AttnParams, ws, dev, backward, where):
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: expected CUDA tensors")
+    if ws is None:
+        return new_attn_workspace(P, dev, backward)
+    if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on {dev}")
+    return ws
+
+
+def _on_device(dev, fn, *args) -> int:
+    """The call with the tensors' device current, on its current stream."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
+
+
+def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, prefix=None, kv_len=None, o=None,
+                    lse=None, ws=None):
+    """Dense attention ``(o, lse)`` of ``q`` [B, Hq, Sq, d] over ``k``, ``v`` [B, Hkv, Skv, d]; the rows are the last
+    ``Sq`` of each entry's ``kv_len`` positions.  ``slopes`` fp32 [Hq]; ``table`` [Hq, buckets] (dtype of q); ``docs``
+    int32 [B, Skv]; ``prefix``, ``kv_len`` int32 [B]."""
+    _check(P._status, "lh_attn_forward")
+    dev = q.device
+    ws = _attn_ws(P, ws, dev, False, "lh_attn_forward")
+    qs, ks = (P.B, P.Hq, P.Sq, P.d), (P.B, P.Hkv, P.Skv, P.d)
+    if o is None:
+        o = torch.empty(qs, dtype=P.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty(qs[:3], dtype=torch.float32, device=dev)
+    mods = _attn_mods(P, dev, slopes, table, docs, prefix, kv_len)
+    rc = _on_device(dev, _lib.lh_attn_forward, P._ref, ctypes.byref(mods),
+                    ctypes.byref(_rows(q, qs, P.dtype, dev, "q")), ctypes.byref(_rows(k, ks, P.dtype, dev, "k")),
+                    ctypes.byref(_rows(v, ks, P.dtype, dev, "v")), ctypes.byref(_rows(o, qs, P.dtype, dev, "o")),
+                    _vec(lse, qs[:3], torch.float32, dev, "lse"), ws.data_ptr(), ws.numel())
+    _check(rc, "lh_attn_forward")
+    return o, lse

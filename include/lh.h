@@ -327,6 +327,69 @@ int lh_cp_backward_attend(const lh_params* P, int G, int rank, const void* dout,
 int lh_cp_backward_unpool(const lh_params* P, int G, int rank, const void* ctx, const float* dkv, void* dq, void* dk,
                           void* dv, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- dense-stage attention ----------------------------------------------------------------------------- */
+
+/* Dense attention of the stage that resumes a model trained with the layer ([W] 深度洞察: the dense recovery stage), and
+ * of its use afterwards: whole sequences, chunks behind a cache, single tokens over a cache.  For row i of a batch
+ * entry, at position x = kv_len - Sq + i, and key j, with query head h reading key head h / (Hq / Hkv):
+ *   z_ij = softcap tanh(scale <q_i, k_j> / softcap)      (softcap 0: scale <q_i, k_j>)
+ *        - slopes[h] |x - j|                             (slopes non-NULL)
+ *        + table[h][bucket(x - j)]                       (table non-NULL; not together with slopes)
+ *   visible(i, j): x >= 0, j < kv_len, docs[x] == docs[j] >= 0, and (causal == 0, or j <= x, or j < prefix)
+ *   o_i = sum_j softmax(z_i)_j v_j over the visible keys, lse_i = ln sum_j exp(z_ij); a row that sees no key gets
+ *   o = 0, lse = -inf and no gradient.
+ * bucket(delta): bidirectional == 0: n = buckets, size = max(delta, 0); else n = buckets / 2, size = |delta|, and n is
+ * added for delta < 0.  With e = n / 2 the first e buckets hold the sizes 0 .. e - 1, bucket b >= e starts at the least
+ * whole size with (size / e)^(n - e) >= (max_distance / e)^(b - e), and the last holds every larger size.
+ * A position with a negative id, a key at or beyond kv_len and a row with x < 0 take part in nothing: whatever their
+ * rows of q, k, v and dout hold (NaN included) reaches no other row.  In the forward the same holds for every masked
+ * pair; in the backward a value that is not finite at a visible position may also reach gradients of rows and keys of
+ * its 128-key and 64-row tiles.
+ * Supported: d in {64, 128}, bf16 or fp16, Hkv | Hq, B Hq <= 65535, Skv <= 2^20, B Hq Sq < 2^31. */
+#define LH_BF16 0
+#define LH_FP16 1
+#define LH_MAX_BUCKETS 128
+
+typedef struct lh_attn_params {
+  int32_t B, Hq, Hkv, Sq, Skv, d; /* all >= 1 */
+  int32_t dtype;                  /* LH_BF16 or LH_FP16: q, k, v, o, table and their gradients */
+  int32_t causal;                 /* 0 or 1 */
+  float scale;                    /* > 0 */
+  float softcap;                  /* >= 0; 0: none */
+  int32_t buckets;                /* columns of the table, 2 .. LH_MAX_BUCKETS (even and >= 4 if bidirectional); 0: none */
+  int32_t max_distance;           /* > n / 2 with n the buckets of one direction (ignored without a table) */
+  int32_t bidirectional;          /* 0 or 1 */
+} lh_attn_params;
+
+/* A [B, H, S, d] tensor: device pointer (16-byte aligned) and strides in elements, positive multiples of 8 (ignored
+ * for a dimension of one); the last dimension is contiguous.  Outputs must not overlap themselves or an input. */
+typedef struct lh_tensor {
+  void* ptr;
+  int64_t stride_b, stride_h, stride_s;
+} lh_tensor;
+
+/* What shapes the scores besides the parameters; device pointers, each may be NULL. */
+typedef struct lh_attn_mods {
+  const float* slopes;    /* [Hq] */
+  const void* table;      /* [Hq, buckets] (dtype); required iff buckets > 0 */
+  const int32_t* docs;    /* [B, Skv] document of each position; NULL: one document */
+  const int32_t* prefix;  /* [B] (causal only) */
+  const int32_t* kv_len;  /* [B], clamped to [0, Skv]; NULL: Skv */
+} lh_attn_mods;
+
+/* LH_OK, LH_ERR_INVALID_ARG or LH_ERR_UNSUPPORTED for the sizes alone. */
+int lh_attn_validate(const lh_attn_params* P);
+
+/* Scratch bytes of lh_attn_forward (backward == 0) or of either call (backward == 1); 0 if invalid. */
+size_t lh_attn_workspace_bytes(const lh_attn_params* P, int backward);
+
+/* First size of each bucket of one direction (the definition above): fills starts[0 .. n - 1] and returns n, or -1. */
+int lh_attn_bucket_starts(const lh_attn_params* P, int32_t* starts);
+
+/* o [B,Hq,Sq,d] and lse (fp32 [B,Hq,Sq]) of q [B,Hq,Sq,d], k, v [B,Hkv,Skv,d].  Bitwise reproducible. */
+int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
+                    const lh_tensor* v, const lh_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- status ------------------------------------------------------------------------------------------ */
 
 /* Synchronises `stream`, returns the first device-side error recorded since the last call (LH_OK if none)
