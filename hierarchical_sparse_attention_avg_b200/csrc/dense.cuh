@@ -122,6 +122,29 @@ int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTens
                      const DenseTensor& v, void* o, const Strides& os, float* lse, const int2* kdoc, float* part_o,
                      float* part_lse, cudaStream_t st);
 
+// Backward: workspace buffers.
+struct DenseBwdBuf {
+  float* stats;         // [2][B Hq][Sq rounded up to 4]: -LSE log2(e) (fp16: + 12; -inf for a dead row), -D
+  unsigned int* amax;   // [B Hkv][2] bits of the largest |dO_i| and |V_j| (fp16 only; zeroed by the caller)
+  float* dqacc;         // fp32 [B Hq][Sq][d]
+  float* dkv;           // fp32 [shares][dV, dK][B Hkv][Skv][d], where the query heads of a key head are shared out
+  const int2 *kdoc, *qdoc;
+  float* bias;          // [Hq][2 near + 1] log2(e) table[h][bucket(delta)], delta = -near .. near
+  uint8_t* bucket;      // [2 near + 1]
+  int2* range;          // [buckets] first and last delta of each bucket
+  float* dtpart;        // [B Hkv][key tiles][G][8 warps][buckets]
+};
+// Blocks that the query heads of one key head are shared out over (dense_bwd.cu).
+int dense_bwd_shares(const DenseDims& a);
+int launch_dense_bwd(const DenseDims& a, const DenseTensor& q, const DenseTensor& k, const DenseTensor& v,
+                     const DenseTensor& dout, const DenseTensor& dk, const DenseTensor& dv, const DenseBwdBuf& w,
+                     cudaStream_t st);
+// dense_prep.cu: the rows' statistics, dqacc = 0 and (fp16) the largest norms; the bias by distance; the results.
+int launch_dense_bwd_rows(const DenseDims& a, const DenseTensor& o, const DenseTensor& dout, const DenseTensor& v,
+                          const float* lse, const DenseBwdBuf& w, cudaStream_t st);
+int launch_dense_bias(const DenseDims& a, const BucketStarts& bs, const DenseBwdBuf& w, cudaStream_t st);
+int launch_dense_bwd_out(const DenseDims& a, const DenseTensor& dq, const DenseTensor& dk, const DenseTensor& dv,
+                         void* dtable, const DenseBwdBuf& w, cudaStream_t st);
 // Device status word of the current device (api.cu).
 int device_status(int** out);
 // 16-bit tensor map over a strided [B,H,S,d] tensor: box {64, pack, rows, 1, 1} of (d, pack, S, H / pack, B).

@@ -49,13 +49,24 @@ void bucket_starts(const lh_attn_params& P, BucketStarts* s) {
   }
 }
 
+// The sizes that the launches and the workspace go by.
+void dense_sizes(const lh_attn_params& P, DenseDims* a, BucketStarts* bs) {
+  memset(a, 0, sizeof(*a));
+  a->B = P.B; a->Hq = P.Hq; a->Hkv = P.Hkv; a->G = P.Hq / P.Hkv; a->Sq = P.Sq; a->Skv = P.Skv; a->d = P.d;
+  a->buckets = P.buckets;
+  bucket_starts(P, bs);
+  if (P.buckets) {  // beyond the last bucket's first size, and beyond the longest distance, nothing changes
+    a->near = bs->start[bs->n - 1];
+    if (a->near > P.Skv + P.Sq) a->near = P.Skv + P.Sq;
+  }
+}
+
 int make_dense(const lh_attn_params* P, const lh_attn_mods* M, DenseDims* a, BucketStarts* bs) {
   const int rc = validate(P);
   if (rc) return rc;
   static const lh_attn_mods none = {};
   if (!M) M = &none;
-  memset(a, 0, sizeof(*a));
-  a->B = P->B; a->Hq = P->Hq; a->Hkv = P->Hkv; a->G = P->Hq / P->Hkv; a->Sq = P->Sq; a->Skv = P->Skv; a->d = P->d;
+  dense_sizes(*P, a, bs);
   a->f16 = P->dtype == LH_FP16;
   a->causal = P->causal;
   a->scale = P->scale;
@@ -65,13 +76,7 @@ int make_dense(const lh_attn_params* P, const lh_attn_mods* M, DenseDims* a, Buc
   if (!aligned4(M->slopes) || !aligned4(M->docs) || !aligned4(M->prefix) || !aligned4(M->kv_len) ||
       ((uintptr_t)M->table & 1u))
     return LH_ERR_INVALID_ARG;
-  a->buckets = P->buckets;
   a->slopes = M->slopes; a->table = M->table; a->docs = M->docs; a->prefix = M->prefix; a->kv_len = M->kv_len;
-  bucket_starts(*P, bs);
-  if (P->buckets) {  // beyond the last bucket's first size, and beyond the longest distance, nothing changes
-    a->near = bs->start[bs->n - 1];
-    if (a->near > P->Skv) a->near = P->Skv;
-  }
   return device_status(&a->status);
 }
 
@@ -89,17 +94,36 @@ bool take(const lh_tensor* t, int B, int H, int S, int d, DenseTensor* out) {
 
 struct DenseWs {
   size_t kdoc, part_o, part_lse, fwd_total;
+  size_t qdoc, stats, amax, dqacc, dkv, bias, bucket, range, dtpart, bwd_total;
 };
 DenseWs dense_ws(const DenseDims& a) {
   DenseWs w;
-  const size_t nk = (a.Skv + kKeyTile - 1) / kKeyTile;
+  const size_t nk = (a.Skv + kKeyTile - 1) / kKeyTile, bhq = (size_t)a.B * a.Hq, bhk = (size_t)a.B * a.Hkv;
   const DenseFwdPlan f = dense_fwd_plan(a);
-  const size_t rows = f.nsplit > 1 ? (size_t)f.nsplit * a.B * a.Hq * a.Sq : 0;
+  const size_t rows = f.nsplit > 1 ? f.nsplit * bhq * a.Sq : 0;
   size_t o = 0;
-  w.kdoc = o; o = align_up(o + (size_t)a.B * nk * sizeof(int2));
-  w.part_o = o; o = align_up(o + rows * a.d * 4);
-  w.part_lse = o; o = align_up(o + rows * 4);
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes);
+    return at;
+  };
+  w.kdoc = take(a.B * nk * sizeof(int2));
+  w.part_o = take(rows * a.d * 4);
+  w.part_lse = take(rows * 4);
   w.fwd_total = o;
+  o = w.part_o;
+  w.qdoc = take((size_t)a.B * ((a.Sq + 63) / 64) * sizeof(int2));
+  w.stats = take(2 * bhq * ((a.Sq + 3) & ~3) * 4);
+  w.amax = take(bhk * 8);
+  w.dqacc = take(bhq * a.Sq * a.d * 4);
+  const int shares = dense_bwd_shares(a);
+  w.dkv = take(shares > 1 ? 2 * shares * bhk * a.Skv * a.d * 4 : 0);
+  const size_t wide = a.buckets ? 2 * (size_t)a.near + 1 : 0;
+  w.bias = take(a.Hq * wide * 4);
+  w.bucket = take(wide);
+  w.range = take(a.buckets * sizeof(int2));
+  w.dtpart = take(bhk * nk * a.G * 8 * a.buckets * 4);
+  w.bwd_total = o;
   return w;
 }
 
@@ -121,11 +145,10 @@ int lh_attn_validate(const lh_attn_params* P) { return validate(P); }
 size_t lh_attn_workspace_bytes(const lh_attn_params* P, int backward) {
   if (validate(P)) return 0;
   DenseDims a;
-  memset(&a, 0, sizeof(a));
-  a.B = P->B; a.Hq = P->Hq; a.Hkv = P->Hkv; a.G = P->Hq / P->Hkv; a.Sq = P->Sq; a.Skv = P->Skv; a.d = P->d;
-  a.buckets = P->buckets;
+  BucketStarts bs;
+  dense_sizes(*P, &a, &bs);
   const DenseWs w = dense_ws(a);
-  return w.fwd_total;
+  return backward && w.bwd_total > w.fwd_total ? w.bwd_total : w.fwd_total;
 }
 
 int lh_attn_bucket_starts(const lh_attn_params* P, int32_t* starts) {
@@ -153,6 +176,43 @@ int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_ten
   if (a.docs) LH_TRY(launch_dense_doc_ranges(a, kdoc, nullptr, st));
   return launch_dense_fwd(a, bs, tq, tk, tv, const_cast<void*>(to.p), to.st, lse, kdoc,
                           reinterpret_cast<float*>(wsb + w.part_o), reinterpret_cast<float*>(wsb + w.part_lse), st);
+}
+
+int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
+                     const lh_tensor* v, const lh_tensor* o, const float* lse, const lh_tensor* dout,
+                     const lh_tensor* dq, const lh_tensor* dk, const lh_tensor* dv, void* dtable, void* ws,
+                     size_t ws_bytes, void* stream) {
+  DenseDims a;
+  BucketStarts bs;
+  LH_TRY(make_dense(P, M, &a, &bs));
+  DenseTensor tq, tk, tv, to, tdo, tdq, tdk, tdv;
+  if (!take(q, a.B, a.Hq, a.Sq, a.d, &tq) || !take(k, a.B, a.Hkv, a.Skv, a.d, &tk) ||
+      !take(v, a.B, a.Hkv, a.Skv, a.d, &tv) || !take(o, a.B, a.Hq, a.Sq, a.d, &to) || !lse || !aligned4(lse) ||
+      !take(dout, a.B, a.Hq, a.Sq, a.d, &tdo) || !take(dq, a.B, a.Hq, a.Sq, a.d, &tdq) ||
+      !take(dk, a.B, a.Hkv, a.Skv, a.d, &tdk) || !take(dv, a.B, a.Hkv, a.Skv, a.d, &tdv) ||
+      (a.table && (!dtable || ((uintptr_t)dtable & 1u))))
+    return LH_ERR_INVALID_ARG;
+  const DenseWs w = dense_ws(a);
+  if (!aligned16(ws) || ws_bytes < w.bwd_total) return ws ? LH_ERR_WORKSPACE : LH_ERR_INVALID_ARG;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  cudaStream_t st = (cudaStream_t)stream;
+  DenseBwdBuf buf;
+  int2 *kdoc = reinterpret_cast<int2*>(wsb + w.kdoc), *qdoc = reinterpret_cast<int2*>(wsb + w.qdoc);
+  buf.stats = reinterpret_cast<float*>(wsb + w.stats);
+  buf.amax = reinterpret_cast<unsigned int*>(wsb + w.amax);
+  buf.dqacc = reinterpret_cast<float*>(wsb + w.dqacc);
+  buf.dkv = reinterpret_cast<float*>(wsb + w.dkv);
+  buf.kdoc = kdoc;
+  buf.qdoc = qdoc;
+  buf.bias = reinterpret_cast<float*>(wsb + w.bias);
+  buf.bucket = wsb + w.bucket;
+  buf.range = reinterpret_cast<int2*>(wsb + w.range);
+  buf.dtpart = reinterpret_cast<float*>(wsb + w.dtpart);
+  if (a.docs) LH_TRY(launch_dense_doc_ranges(a, kdoc, qdoc, st));
+  if (a.table) LH_TRY(launch_dense_bias(a, bs, buf, st));
+  LH_TRY(launch_dense_bwd_rows(a, to, tdo, tv, lse, buf, st));
+  LH_TRY(launch_dense_bwd(a, tq, tk, tv, tdo, tdk, tdv, buf, st));
+  return launch_dense_bwd_out(a, tdq, tdk, tdv, dtable, buf, st);
 }
 
 }  // extern "C"

@@ -98,6 +98,7 @@ _SIGS = {
     "lh_attn_workspace_bytes": (ctypes.c_size_t, [_vp, ctypes.c_int]),
     "lh_attn_bucket_starts": (ctypes.c_int, [_vp, _vp]),
     "lh_attn_forward": (ctypes.c_int, [_vp] * 8 + [ctypes.c_size_t, _vp]),
+    "lh_attn_backward": (ctypes.c_int, [_vp] * 13 + [ctypes.c_size_t, _vp]),
 }
 
 
@@ -611,3 +612,27 @@ def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, 
                     _vec(lse, qs[:3], torch.float32, dev, "lse"), ws.data_ptr(), ws.numel())
     _check(rc, "lh_attn_forward")
     return o, lse
+
+
+def lh_attn_backward(P: AttnParams, q, k, v, o, lse, dout, slopes=None, table=None, docs=None, prefix=None, kv_len=None,
+                     dq=None, dk=None, dv=None, dtable=None, ws=None):
+    """Gradients ``(dq, dk, dv, dtable)`` of ``lh_attn_forward`` (``dtable`` None without a table); ``o`` and ``lse`` are
+    its results, the other arguments those it got.  ``ws``: from ``new_attn_workspace(..., backward=True)``."""
+    _check(P._status, "lh_attn_backward")
+    dev = q.device
+    ws = _attn_ws(P, ws, dev, True, "lh_attn_backward")
+    qs, ks = (P.B, P.Hq, P.Sq, P.d), (P.B, P.Hkv, P.Skv, P.d)
+    dq = torch.empty(qs, dtype=P.dtype, device=dev) if dq is None else dq
+    dk = torch.empty(ks, dtype=P.dtype, device=dev) if dk is None else dk
+    dv = torch.empty(ks, dtype=P.dtype, device=dev) if dv is None else dv
+    if P.buckets and dtable is None:
+        dtable = torch.empty((P.Hq, P.buckets), dtype=P.dtype, device=dev)
+    mods = _attn_mods(P, dev, slopes, table, docs, prefix, kv_len)
+    t = [ctypes.byref(_rows(x, s, P.dtype, dev, n)) for x, s, n in
+         ((q, qs, "q"), (k, ks, "k"), (v, ks, "v"), (o, qs, "o"), (dout, qs, "dout"), (dq, qs, "dq"), (dk, ks, "dk"),
+          (dv, ks, "dv"))]
+    rc = _on_device(dev, _lib.lh_attn_backward, P._ref, ctypes.byref(mods), t[0], t[1], t[2], t[3],
+                    _vec(lse, qs[:3], torch.float32, dev, "lse"), t[4], t[5], t[6], t[7],
+                    _vec(dtable, (P.Hq, P.buckets), P.dtype, dev, "dtable"), ws.data_ptr(), ws.numel())
+    _check(rc, "lh_attn_backward")
+    return dq, dk, dv, dtable

@@ -390,6 +390,14 @@ int lh_attn_bucket_starts(const lh_attn_params* P, int32_t* starts);
 int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
                     const lh_tensor* v, const lh_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* Gradients of the call above for dout [B,Hq,Sq,d]: dq, dk, dv of their tensors' shapes (a shared key head's over all of
+ * its query heads) and, with a table, dtable [Hq, buckets].  q, k, v, M as in the forward; o and lse its results.  dk, dv
+ * and dtable are bitwise reproducible; dq is accumulated with fp32 reduce-adds in no fixed order before it is rounded. */
+int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
+                     const lh_tensor* v, const lh_tensor* o, const float* lse, const lh_tensor* dout,
+                     const lh_tensor* dq, const lh_tensor* dk, const lh_tensor* dv, void* dtable, void* ws,
+                     size_t ws_bytes, void* stream);
+
 /* ---- status ------------------------------------------------------------------------------------------ */
 
 /* Synchronises `stream`, returns the first device-side error recorded since the last call (LH_OK if none)

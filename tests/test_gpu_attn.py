@@ -82,6 +82,16 @@ FORWARD = {
 }
 
 
+BACKWARD = {n: FORWARD[n] for n in FORWARD if n not in ("long_cache", "wide_grid")}
+BACKWARD.update({
+    "group8": (dict(B=1, Hq=8, Hkv=1, Sq=700, Skv=700, d=128, softcap=50.0), dict(docs=[spans(700, 300, 350)])),
+    "longer": (dict(B=1, Hq=2, Hkv=2, Sq=2100, Skv=2100, d=64, dtype=FP), {}),
+    "bias_longer": (dict(B=2, Hq=2, Hkv=1, Sq=1500, Skv=1500, d=128, buckets=32, max_distance=128), {}),
+    "bias_wide": (dict(B=1, Hq=2, Hkv=2, Sq=1500, Skv=1500, d=64, buckets=48, max_distance=1000, bidirectional=True,
+                       causal=False, dtype=FP), {}),
+})
+
+
 @pytest.mark.parametrize("name", FORWARD)
 def test_forward(lh, cuda_device, name):
     p, m = FORWARD[name]
@@ -95,3 +105,22 @@ def test_forward(lh, cuda_device, name):
     A.check("o", o, ref)
     o2, lse2 = lh.lh_attn_forward(P, q, k, v, **m)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)  # no order left open
+
+
+@pytest.mark.parametrize("name", BACKWARD)
+def test_backward(lh, cuda_device, name):
+    p, m = BACKWARD[name]
+    P = lh.AttnParams(**p)
+    q, k, v, dout = A.make(P, 3, cuda_device, grad=True)
+    m = mods(P, cuda_device, **m)
+    o, lse = lh.lh_attn_forward(P, q, k, v, **m)
+    grads = lh.lh_attn_backward(P, q, k, v, o, lse, dout, **m)
+    assert lh.lh_get_status() == lh.LH_OK
+    ref = A.reference(P, q, k, v, dout=dout, **m)
+    names = ("dq", "dk", "dv") + (("dtable",) if P.buckets else ())
+    assert len(grads) == 4 and (P.buckets or grads[3] is None)
+    for n, g in zip(names, grads):
+        A.check(n, g, ref)
+    again = lh.lh_attn_backward(P, q, k, v, o, lse, dout, **m)
+    for n, g, g2 in zip(names[1:], grads[1:], again[1:]):  # (dq's fp32 sums have no fixed order)
+        assert torch.equal(g, g2), n
