@@ -100,6 +100,20 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return F16 ? (((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u) : (((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u);
 }
 
+// o's 16-bit row chunk of 8 features, and what its rounding dropped (low may be null).
+template <bool F16>
+__device__ __forceinline__ void store8(uint16_t* o, uint16_t* low, const float* v) {
+  uint32_t w[4], r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = pack2_rn<F16>(v[2 * i], v[2 * i + 1]);
+    const float2 u = unpack2<F16>(w[i]);
+    r[i] = pack2_rn<F16>(v[2 * i] - u.x, v[2 * i + 1] - u.y);
+  }
+  st16(o, make_uint4(w[0], w[1], w[2], w[3]));
+  if (low) st16(low, make_uint4(r[0], r[1], r[2], r[3]));
+}
+
 // ---- launches (each in the file it names) ----------------------------------------------------------------
 // A [B,H,S,d] tensor with unit feature stride.
 struct DenseTensor {
@@ -117,10 +131,10 @@ DenseFwdPlan dense_fwd_plan(const DenseDims& a);
 // dense_prep.cu: ids' range (min, max) of every key tile: kdoc [B][ceil(Skv / 128)]; with qdoc, of every 64-row
 // sub-tile of the queries too: qdoc [B][ceil(Sq / 64)].
 int launch_dense_doc_ranges(const DenseDims& a, int2* kdoc, int2* qdoc, cudaStream_t st);
-// dense_fwd.cu: part_o / part_lse: nsplit > 1 only.
+// dense_fwd.cu: low.p may be null; part_o / part_lse: nsplit > 1 only.
 int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTensor& q, const DenseTensor& k,
-                     const DenseTensor& v, void* o, const Strides& os, float* lse, const int2* kdoc, float* part_o,
-                     float* part_lse, cudaStream_t st);
+                     const DenseTensor& v, const DenseTensor& o, const DenseTensor& low, float* lse, const int2* kdoc,
+                     float* part_o, float* part_lse, cudaStream_t st);
 
 // Backward: workspace buffers.
 struct DenseBwdBuf {
@@ -140,8 +154,8 @@ int launch_dense_bwd(const DenseDims& a, const DenseTensor& q, const DenseTensor
                      const DenseTensor& dout, const DenseTensor& dk, const DenseTensor& dv, const DenseBwdBuf& w,
                      cudaStream_t st);
 // dense_prep.cu: the rows' statistics, dqacc = 0 and (fp16) the largest norms; the bias by distance; the results.
-int launch_dense_bwd_rows(const DenseDims& a, const DenseTensor& o, const DenseTensor& dout, const DenseTensor& v,
-                          const float* lse, const DenseBwdBuf& w, cudaStream_t st);
+int launch_dense_bwd_rows(const DenseDims& a, const DenseTensor& o, const DenseTensor& low, const DenseTensor& dout,
+                          const DenseTensor& v, const float* lse, const DenseBwdBuf& w, cudaStream_t st);
 int launch_dense_bias(const DenseDims& a, const BucketStarts& bs, const DenseBwdBuf& w, cudaStream_t st);
 int launch_dense_bwd_out(const DenseDims& a, const DenseTensor& dq, const DenseTensor& dk, const DenseTensor& dv,
                          void* dtable, const DenseBwdBuf& w, cudaStream_t st);

@@ -160,13 +160,15 @@ int lh_attn_bucket_starts(const lh_attn_params* P, int32_t* starts) {
 }
 
 int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
-                    const lh_tensor* v, const lh_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+                    const lh_tensor* v, const lh_tensor* o, const lh_tensor* low, float* lse, void* ws, size_t ws_bytes,
+                    void* stream) {
   DenseDims a;
   BucketStarts bs;
   LH_TRY(make_dense(P, M, &a, &bs));
-  DenseTensor tq, tk, tv, to;
+  DenseTensor tq, tk, tv, to, tl = {nullptr, {0, 0, 0}};
   if (!take(q, a.B, a.Hq, a.Sq, a.d, &tq) || !take(k, a.B, a.Hkv, a.Skv, a.d, &tk) ||
-      !take(v, a.B, a.Hkv, a.Skv, a.d, &tv) || !take(o, a.B, a.Hq, a.Sq, a.d, &to) || !lse || !aligned4(lse))
+      !take(v, a.B, a.Hkv, a.Skv, a.d, &tv) || !take(o, a.B, a.Hq, a.Sq, a.d, &to) ||
+      (low && !take(low, a.B, a.Hq, a.Sq, a.d, &tl)) || !lse || !aligned4(lse))
     return LH_ERR_INVALID_ARG;
   const DenseWs w = dense_ws(a);
   if (!aligned16(ws) || ws_bytes < w.fwd_total) return ws ? LH_ERR_WORKSPACE : LH_ERR_INVALID_ARG;
@@ -174,20 +176,21 @@ int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_ten
   cudaStream_t st = (cudaStream_t)stream;
   int2* kdoc = reinterpret_cast<int2*>(wsb + w.kdoc);
   if (a.docs) LH_TRY(launch_dense_doc_ranges(a, kdoc, nullptr, st));
-  return launch_dense_fwd(a, bs, tq, tk, tv, const_cast<void*>(to.p), to.st, lse, kdoc,
+  return launch_dense_fwd(a, bs, tq, tk, tv, to, tl, lse, kdoc,
                           reinterpret_cast<float*>(wsb + w.part_o), reinterpret_cast<float*>(wsb + w.part_lse), st);
 }
 
 int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
-                     const lh_tensor* v, const lh_tensor* o, const float* lse, const lh_tensor* dout,
-                     const lh_tensor* dq, const lh_tensor* dk, const lh_tensor* dv, void* dtable, void* ws,
+                     const lh_tensor* v, const lh_tensor* o, const lh_tensor* low, const float* lse,
+                     const lh_tensor* dout, const lh_tensor* dq, const lh_tensor* dk, const lh_tensor* dv, void* dtable, void* ws,
                      size_t ws_bytes, void* stream) {
   DenseDims a;
   BucketStarts bs;
   LH_TRY(make_dense(P, M, &a, &bs));
-  DenseTensor tq, tk, tv, to, tdo, tdq, tdk, tdv;
+  DenseTensor tq, tk, tv, to, tl = {nullptr, {0, 0, 0}}, tdo, tdq, tdk, tdv;
   if (!take(q, a.B, a.Hq, a.Sq, a.d, &tq) || !take(k, a.B, a.Hkv, a.Skv, a.d, &tk) ||
-      !take(v, a.B, a.Hkv, a.Skv, a.d, &tv) || !take(o, a.B, a.Hq, a.Sq, a.d, &to) || !lse || !aligned4(lse) ||
+      !take(v, a.B, a.Hkv, a.Skv, a.d, &tv) || !take(o, a.B, a.Hq, a.Sq, a.d, &to) ||
+      (low && !take(low, a.B, a.Hq, a.Sq, a.d, &tl)) || !lse || !aligned4(lse) ||
       !take(dout, a.B, a.Hq, a.Sq, a.d, &tdo) || !take(dq, a.B, a.Hq, a.Sq, a.d, &tdq) ||
       !take(dk, a.B, a.Hkv, a.Skv, a.d, &tdk) || !take(dv, a.B, a.Hkv, a.Skv, a.d, &tdv) ||
       (a.table && (!dtable || ((uintptr_t)dtable & 1u))))
@@ -210,7 +213,7 @@ int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_te
   buf.dtpart = reinterpret_cast<float*>(wsb + w.dtpart);
   if (a.docs) LH_TRY(launch_dense_doc_ranges(a, kdoc, qdoc, st));
   if (a.table) LH_TRY(launch_dense_bias(a, bs, buf, st));
-  LH_TRY(launch_dense_bwd_rows(a, to, tdo, tv, lse, buf, st));
+  LH_TRY(launch_dense_bwd_rows(a, to, tl, tdo, tv, lse, buf, st));
   LH_TRY(launch_dense_bwd(a, tq, tk, tv, tdo, tdk, tdv, buf, st));
   return launch_dense_bwd_out(a, tdq, tdk, tdv, dtable, buf, st);
 }

@@ -54,8 +54,7 @@ struct FwdArgs {
   uint32_t off_k, off_v, off_bar, off_ids, off_win, off_flags;
   int win;  // floats of one stream's bias window
   DenseTensor v;
-  void* o;
-  Strides os;
+  DenseTensor o, low;
   float* lse;
   const int2* kdoc;
   float *part_o, *part_lse;
@@ -530,7 +529,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t ri = ((int64_t)b * a.Hq + h) * a.Sq + tk;
         const bool part = p.nsplit > 1;
         const int64_t pi = (int64_t)split * a.B * a.Hq * a.Sq + ri;
-        uint16_t* orow = static_cast<uint16_t*>(p.o) + b * p.os.b + h * p.os.h + (int64_t)tk * p.os.s;
+        auto at = [&](const DenseTensor& t) {
+          return static_cast<uint16_t*>(const_cast<void*>(t.p)) + b * t.st.b + h * t.st.h + (int64_t)tk * t.st.s;
+        };
+        uint16_t *orow = at(p.o), *lrow = p.low.p ? at(p.low) : nullptr;
         float* prow = part ? p.part_o + pi * D : nullptr;
         const bool use1 = p.dual && a1 != 0.f;
         const float c0 = cnt > 0 ? a0 * inv : 0.f, c1 = a1 * inv;
@@ -555,9 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(orow + c * 32 + i) =
-                    make_uint4(pack2_rn<F16>(o[i], o[i + 1]), pack2_rn<F16>(o[i + 2], o[i + 3]),
-                               pack2_rn<F16>(o[i + 4], o[i + 5]), pack2_rn<F16>(o[i + 6], o[i + 7]));
+                store8<F16>(orow + c * 32 + i, lrow ? lrow + c * 32 + i : nullptr, o + i);
             }
           }
         }
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // nsplit (d + 1) floats a row; latency-bound (a few rows per SM).
 template <int D, bool F16>
 __global__ void __launch_bounds__(128) join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                                                   void* __restrict__ o, Strides os, float* __restrict__ lse, int nsplit,
+                                                   DenseTensor o, DenseTensor low, float* __restrict__ lse, int nsplit,
                                                    int64_t rows, int Hq, int Sq) {
   const int64_t row = blockIdx.x;
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -628,13 +628,16 @@ __global__ void __launch_bounds__(128) join_kernel(const float* __restrict__ par
   __syncthreads();
   const float lt = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]), inv = lt == 0.f ? 0.f : 1.0f / lt;
   const int64_t tk = row % Sq, bh = row / Sq, h = bh % Hq, b = bh / Hq;
-  uint16_t* orow = static_cast<uint16_t*>(o) + b * os.b + h * os.h + tk * os.s;
-  for (int i = threadIdx.x; i < D / 2; i += 128) {
-    float v[2];
+  auto at = [&](const DenseTensor& t) {
+    return static_cast<uint16_t*>(const_cast<void*>(t.p)) + b * t.st.b + h * t.st.h + tk * t.st.s;
+  };
+  const int i = threadIdx.x * 8;
+  if (i < D) {
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      v[e] = ((s_acc[0][2 * i + e] + s_acc[1][2 * i + e]) + (s_acc[2][2 * i + e] + s_acc[3][2 * i + e])) * inv;
-    reinterpret_cast<uint32_t*>(orow)[i] = pack2_rn<F16>(v[0], v[1]);
+    for (int e = 0; e < 8; ++e)
+      v[e] = ((s_acc[0][i + e] + s_acc[1][i + e]) + (s_acc[2][i + e] + s_acc[3][i + e])) * inv;
+    store8<F16>(at(o) + i, low.p ? at(low) + i : nullptr, v);
   }
   if (threadIdx.x == 0) lse[row] = lt == 0.f ? -INFINITY : (m + __log2f(lt)) * kLn2;
 }
@@ -690,8 +693,8 @@ DenseFwdPlan dense_fwd_plan(const DenseDims& a) {
 }
 
 int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTensor& q, const DenseTensor& k,
-                     const DenseTensor& v, void* o, const Strides& os, float* lse, const int2* kdoc, float* part_o,
-                     float* part_lse, cudaStream_t st) {
+                     const DenseTensor& v, const DenseTensor& o, const DenseTensor& low, float* lse, const int2* kdoc,
+                     float* part_o, float* part_lse, cudaStream_t st) {
   const DenseFwdPlan f = dense_fwd_plan(a);
   CUtensorMap mq, mk, mv;
   if (make_tmap_dense(&mq, q, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok) ||
@@ -718,7 +721,7 @@ int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTens
   p.off_flags = p.off_win + 2 * p.win * 4;
   p.v = v;
   p.o = o;
-  p.os = os;
+  p.low = low;
   p.lse = lse;
   p.kdoc = kdoc;
   p.part_o = part_o;
@@ -737,7 +740,7 @@ int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTens
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
   auto join = a.d == 64 ? (a.f16 ? join_kernel<64, true> : join_kernel<64, false>)
                         : (a.f16 ? join_kernel<128, true> : join_kernel<128, false>);
-  join<<<(unsigned)rows, 128, 0, st>>>(part_o, part_lse, o, os, lse, f.nsplit, rows, a.Hq, a.Sq);
+  join<<<(unsigned)rows, 128, 0, st>>>(part_o, part_lse, o, low, lse, f.nsplit, rows, a.Hq, a.Sq);
   return check_launch();
 }
 

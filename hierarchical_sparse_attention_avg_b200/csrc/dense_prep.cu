@@ -31,8 +31,8 @@ __global__ void doc_ranges_kernel(const DenseDims a, int2* __restrict__ kdoc, in
 // fp16 the largest |dO_i| of the key head's rows (one atomicMax of a bit pattern per block: order-free).
 template <int D, bool F16>
 __global__ void __launch_bounds__(256)
-    bwd_rows_kernel(const DenseDims a, const uint16_t* __restrict__ o, Strides os, const uint16_t* __restrict__ dout,
-                    Strides ds, const float* __restrict__ lse, float* __restrict__ stats, float* __restrict__ dqacc,
+    bwd_rows_kernel(const DenseDims a, const uint16_t* __restrict__ o, Strides os, const uint16_t* __restrict__ low,
+                    Strides ls, const uint16_t* __restrict__ dout, Strides ds, const float* __restrict__ lse, float* __restrict__ stats, float* __restrict__ dqacc,
                     unsigned int* __restrict__ amax) {
   constexpr int L = D / 8, ROWS = 256 / L;
   const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq;
@@ -42,11 +42,12 @@ __global__ void __launch_bounds__(256)
   if (in) {
     const uint4 x = ld16(o + b * os.b + h * os.h + (int64_t)i * os.s + f);
     const uint4 y = ld16(dout + b * ds.b + h * ds.h + (int64_t)i * ds.s + f);
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+    const uint4 z = low ? ld16(low + b * ls.b + h * ls.h + (int64_t)i * ls.s + f) : make_uint4(0, 0, 0, 0);
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w}, zw[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 u = unpack2<F16>(xw[e]), w = unpack2<F16>(yw[e]);
-      dot = fmaf(u.x, w.x, fmaf(u.y, w.y, dot));
+      const float2 u = unpack2<F16>(xw[e]), w = unpack2<F16>(yw[e]), r = unpack2<F16>(zw[e]);
+      dot = fmaf(u.x + r.x, w.x, fmaf(u.y + r.y, w.y, dot));
       norm = fmaf(w.x, w.x, fmaf(w.y, w.y, norm));
     }
     float4* acc = reinterpret_cast<float4*>(dqacc + ((int64_t)bh * a.Sq + i) * D + f);
@@ -171,13 +172,14 @@ __global__ void __launch_bounds__(256) dtable_kernel(const DenseDims a, const fl
 }
 
 template <int D, bool F16>
-int rows_t(const DenseDims& a, const DenseTensor& o, const DenseTensor& dout, const DenseTensor& v, const float* lse,
+int rows_t(const DenseDims& a, const DenseTensor& o, const DenseTensor& low, const DenseTensor& dout, const DenseTensor& v, const float* lse,
            const DenseBwdBuf& w, cudaStream_t st) {
   constexpr int ROWS = 256 / (D / 8);
   KernelTimer timer("dense_bwd_rows", st);
   if (F16 && cudaMemsetAsync(w.amax, 0, (size_t)a.B * a.Hkv * 8, st) != cudaSuccess) return LH_ERR_CUDA;
   bwd_rows_kernel<D, F16><<<dim3((a.Sq + ROWS - 1) / ROWS, a.B * a.Hq), 256, 0, st>>>(
-      a, static_cast<const uint16_t*>(o.p), o.st, static_cast<const uint16_t*>(dout.p), dout.st, lse, w.stats, w.dqacc,
+      a, static_cast<const uint16_t*>(o.p), o.st, static_cast<const uint16_t*>(low.p), low.st,
+      static_cast<const uint16_t*>(dout.p), dout.st, lse, w.stats, w.dqacc,
       w.amax);
   if (F16)
     v_norm_kernel<D><<<dim3((a.Skv + 8 * ROWS - 1) / (8 * ROWS), a.B * a.Hkv), 256, 0, st>>>(
@@ -209,10 +211,10 @@ int out_t(const DenseDims& a, const DenseTensor& dq, const DenseTensor& dk, cons
 
 }  // namespace
 
-int launch_dense_bwd_rows(const DenseDims& a, const DenseTensor& o, const DenseTensor& dout, const DenseTensor& v,
-                          const float* lse, const DenseBwdBuf& w, cudaStream_t st) {
-  return a.d == 64 ? (a.f16 ? rows_t<64, true>(a, o, dout, v, lse, w, st) : rows_t<64, false>(a, o, dout, v, lse, w, st))
-                   : (a.f16 ? rows_t<128, true>(a, o, dout, v, lse, w, st) : rows_t<128, false>(a, o, dout, v, lse, w, st));
+int launch_dense_bwd_rows(const DenseDims& a, const DenseTensor& o, const DenseTensor& low, const DenseTensor& dout,
+                          const DenseTensor& v, const float* lse, const DenseBwdBuf& w, cudaStream_t st) {
+  auto run = a.d == 64 ? (a.f16 ? rows_t<64, true> : rows_t<64, false>) : (a.f16 ? rows_t<128, true> : rows_t<128, false>);
+  return run(a, o, low, dout, v, lse, w, st);
 }
 
 int launch_dense_bias(const DenseDims& a, const BucketStarts& bs, const DenseBwdBuf& w, cudaStream_t st) {

@@ -97,8 +97,8 @@ _SIGS = {
     "lh_attn_validate": (ctypes.c_int, [_vp]),
     "lh_attn_workspace_bytes": (ctypes.c_size_t, [_vp, ctypes.c_int]),
     "lh_attn_bucket_starts": (ctypes.c_int, [_vp, _vp]),
-    "lh_attn_forward": (ctypes.c_int, [_vp] * 8 + [ctypes.c_size_t, _vp]),
-    "lh_attn_backward": (ctypes.c_int, [_vp] * 13 + [ctypes.c_size_t, _vp]),
+    "lh_attn_forward": (ctypes.c_int, [_vp] * 9 + [ctypes.c_size_t, _vp]),
+    "lh_attn_backward": (ctypes.c_int, [_vp] * 14 + [ctypes.c_size_t, _vp]),
 }
 
 
@@ -593,10 +593,11 @@ def _on_device(dev, fn, *args) -> int:
 
 
 def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, prefix=None, kv_len=None, o=None,
-                    lse=None, ws=None):
+                    lse=None, low=None, ws=None):
     """Dense attention ``(o, lse)`` of ``q`` [B, Hq, Sq, d] over ``k``, ``v`` [B, Hkv, Skv, d]; the rows are the last
     ``Sq`` of each entry's ``kv_len`` positions.  ``slopes`` fp32 [Hq]; ``table`` [Hq, buckets] (dtype of q); ``docs``
-    int32 [B, Skv]; ``prefix``, ``kv_len`` int32 [B]."""
+    int32 [B, Skv]; ``prefix``, ``kv_len`` int32 [B].  ``low`` (like ``o``): receives what o's rounding dropped; handed to
+    ``lh_attn_backward`` it makes the gradients about twice as exact."""
     _check(P._status, "lh_attn_forward")
     dev = q.device
     ws = _attn_ws(P, ws, dev, False, "lh_attn_forward")
@@ -609,15 +610,16 @@ def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, 
     rc = _on_device(dev, _lib.lh_attn_forward, P._ref, ctypes.byref(mods),
                     ctypes.byref(_rows(q, qs, P.dtype, dev, "q")), ctypes.byref(_rows(k, ks, P.dtype, dev, "k")),
                     ctypes.byref(_rows(v, ks, P.dtype, dev, "v")), ctypes.byref(_rows(o, qs, P.dtype, dev, "o")),
+                    None if low is None else ctypes.byref(_rows(low, qs, P.dtype, dev, "low")),
                     _vec(lse, qs[:3], torch.float32, dev, "lse"), ws.data_ptr(), ws.numel())
     _check(rc, "lh_attn_forward")
     return o, lse
 
 
 def lh_attn_backward(P: AttnParams, q, k, v, o, lse, dout, slopes=None, table=None, docs=None, prefix=None, kv_len=None,
-                     dq=None, dk=None, dv=None, dtable=None, ws=None):
-    """Gradients ``(dq, dk, dv, dtable)`` of ``lh_attn_forward`` (``dtable`` None without a table); ``o`` and ``lse`` are
-    its results, the other arguments those it got.  ``ws``: from ``new_attn_workspace(..., backward=True)``."""
+                     low=None, dq=None, dk=None, dv=None, dtable=None, ws=None):
+    """Gradients ``(dq, dk, dv, dtable)`` of ``lh_attn_forward`` (``dtable`` None without a table); ``o``, ``lse`` and
+    ``low`` are its results, the other arguments those it got.  ``ws``: from ``new_attn_workspace(..., backward=True)``."""
     _check(P._status, "lh_attn_backward")
     dev = q.device
     ws = _attn_ws(P, ws, dev, True, "lh_attn_backward")
@@ -632,7 +634,7 @@ def lh_attn_backward(P: AttnParams, q, k, v, o, lse, dout, slopes=None, table=No
          ((q, qs, "q"), (k, ks, "k"), (v, ks, "v"), (o, qs, "o"), (dout, qs, "dout"), (dq, qs, "dq"), (dk, ks, "dk"),
           (dv, ks, "dv"))]
     rc = _on_device(dev, _lib.lh_attn_backward, P._ref, ctypes.byref(mods), t[0], t[1], t[2], t[3],
-                    _vec(lse, qs[:3], torch.float32, dev, "lse"), t[4], t[5], t[6], t[7],
+                    None if low is None else ctypes.byref(_rows(low, qs, P.dtype, dev, "low")), _vec(lse, qs[:3], torch.float32, dev, "lse"), t[4], t[5], t[6], t[7],
                     _vec(dtable, (P.Hq, P.buckets), P.dtype, dev, "dtable"), ws.data_ptr(), ws.numel())
     _check(rc, "lh_attn_backward")
     return dq, dk, dv, dtable

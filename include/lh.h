@@ -386,16 +386,21 @@ size_t lh_attn_workspace_bytes(const lh_attn_params* P, int backward);
 /* First size of each bucket of one direction (the definition above): fills starts[0 .. n - 1] and returns n, or -1. */
 int lh_attn_bucket_starts(const lh_attn_params* P, int32_t* starts);
 
-/* o [B,Hq,Sq,d] and lse (fp32 [B,Hq,Sq]) of q [B,Hq,Sq,d], k, v [B,Hkv,Skv,d].  Bitwise reproducible. */
+/* o [B,Hq,Sq,d] and lse (fp32 [B,Hq,Sq]) of q [B,Hq,Sq,d], k, v [B,Hkv,Skv,d].  Bitwise reproducible.
+ * low: NULL, or a tensor of o's shape that receives what o's rounding dropped (dtype), for the backward. */
 int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
-                    const lh_tensor* v, const lh_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+                    const lh_tensor* v, const lh_tensor* o, const lh_tensor* low, float* lse, void* ws, size_t ws_bytes,
+                    void* stream);
 
 /* Gradients of the call above for dout [B,Hq,Sq,d]: dq, dk, dv of their tensors' shapes (a shared key head's over all of
- * its query heads) and, with a table, dtable [Hq, buckets].  q, k, v, M as in the forward; o and lse its results.  dk, dv
- * and dtable are bitwise reproducible; dq is accumulated with fp32 reduce-adds in no fixed order before it is rounded. */
+ * its query heads) and, with a table, dtable [Hq, buckets].  q, k, v, M as in the forward; o and lse its results.  low:
+ * NULL, or the forward's: dZ = P (dP - <dout, o>) takes a small difference, so o's own rounding is the largest error of
+ * the gradients without it (bf16: dq, dk 2.4e-3 off the formula in the 2-norm with it, 4.2e-3 without, dtable up to
+ * 7e-3).  dk, dv and dtable are bitwise reproducible; dq is accumulated with fp32 reduce-adds in no fixed order before
+ * it is rounded. */
 int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
-                     const lh_tensor* v, const lh_tensor* o, const float* lse, const lh_tensor* dout,
-                     const lh_tensor* dq, const lh_tensor* dk, const lh_tensor* dv, void* dtable, void* ws,
+                     const lh_tensor* v, const lh_tensor* o, const lh_tensor* low, const float* lse,
+                     const lh_tensor* dout, const lh_tensor* dq, const lh_tensor* dk, const lh_tensor* dv, void* dtable, void* ws,
                      size_t ws_bytes, void* stream);
 
 /* ---- status ------------------------------------------------------------------------------------------ */

@@ -4,7 +4,7 @@ Bounds count the roundings of the kernels' number formats, u = finfo(dtype).eps 
 the 32-bit sums and exponentials (EPS32):
   o: the probabilities are rounded once before P V, the result once:      u |o| + (u + EPS32) P|V|
   dV: P rounded, the result rounded:                                      u |dV| + (u + EPS32) P^T|dO|
-  dZ: D = <dO, O> uses the rounded O (u) of rounded probabilities (u):    eD = (2 u + EPS32) |dO|.(P|V|), P eD
+  dZ: D = <dO, O> uses O of rounded probabilities (u), rounded (u, or u^2 with `low`): eD = (2 u + EPS32) |dO|.(P|V|), P eD
   dK: dS rounded, D's error, the result rounded:                          u |dK| + scale ((u + EPS32) |dS| + P eD)^T |Q|
   dQ: likewise over the keys.   dtable: sums of dZ in 32 bits, D's error, the result rounded.
 EPS32: scores are fp32 sums of d <= 128 products (d 2^-24 of |q||k| scale, measured there as `ez`), exponentials 2^-22."""
@@ -16,6 +16,10 @@ import math
 import torch
 
 F8 = torch.float64
+
+
+def half_step(P) -> float:
+    return torch.finfo(P.dtype).eps / 2
 
 
 def bucket_index(far: torch.Tensor, buckets: int, distance: int, both: bool) -> torch.Tensor:
@@ -48,7 +52,7 @@ def visible(B, Sq, Skv, causal, docs=None, prefix=None, kv_len=None):
     return x, m
 
 
-def reference(P, q, k, v, slopes=None, table=None, docs=None, prefix=None, kv_len=None, dout=None):
+def reference(P, q, k, v, slopes=None, table=None, docs=None, prefix=None, kv_len=None, low=None, dout=None):
     """dict of o, lse (and dq, dk, dv, dtable) in float64, each with its bound e_*."""
     dev, G = q.device, P.Hq // P.Hkv
     u, eps = torch.finfo(P.dtype).eps / 2, 2.0 ** -14
@@ -84,7 +88,7 @@ def reference(P, q, k, v, slopes=None, table=None, docs=None, prefix=None, kv_le
     dv, e_dv = p.transpose(2, 3) @ W, p.transpose(2, 3) @ W.abs()
     dp = W @ V.transpose(2, 3)
     dz = p * (dp - (W * o).sum(3, keepdim=True))
-    eD = ((2 * u + eps) * (W.abs() * pv).sum(3, keepdim=True))
+    eD = (((u + u * u if low is not None else 2 * u) + eps) * (W.abs() * pv).sum(3, keepdim=True))
     ep = (2.0 ** -16 + 2 * ez[..., None])  # relative error of p, and of dP against its products' size
     e_dz = p * eD + ep * p * (dp.abs() + (W.abs() * pv).sum(3, keepdim=True)) + p * (
         2.0 ** -17 * W.norm(dim=3)[..., None] * V.norm(dim=3)[:, :, None])

@@ -107,16 +107,21 @@ def test_forward(lh, cuda_device, name):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)  # no order left open
 
 
+@pytest.mark.parametrize("exact", [False, True], ids=["o", "o_low"])
 @pytest.mark.parametrize("name", BACKWARD)
-def test_backward(lh, cuda_device, name):
+def test_backward(lh, cuda_device, name, exact):
     p, m = BACKWARD[name]
     P = lh.AttnParams(**p)
     q, k, v, dout = A.make(P, 3, cuda_device, grad=True)
     m = mods(P, cuda_device, **m)
-    o, lse = lh.lh_attn_forward(P, q, k, v, **m)
+    low = torch.empty_like(q) if exact else None
+    o, lse = lh.lh_attn_forward(P, q, k, v, low=low, **m)
+    m["low"] = low
     grads = lh.lh_attn_backward(P, q, k, v, o, lse, dout, **m)
     assert lh.lh_get_status() == lh.LH_OK
     ref = A.reference(P, q, k, v, dout=dout, **m)
+    if exact:  # low is a second rounding's remainder
+        assert ((o.double() + low.double() - ref["o"]).abs() <= ref["e_o"] - A.half_step(P) * ref["o"].abs() * 0.99 + 1e-7).all()
     names = ("dq", "dk", "dv") + (("dtable",) if P.buckets else ())
     assert len(grads) == 4 and (P.buckets or grads[3] is None)
     for n, g in zip(names, grads):
