@@ -13,6 +13,9 @@ namespace lh {
 constexpr int kMaxBuckets = 128;       // columns of the bias table
 constexpr int kMaxDenseKeys = 1 << 20; // keys per head (one flag byte per 128-key tile in shared memory)
 constexpr int kKeyTile = 128;
+// Up to this many key tiles the forward's blocks take the ids' ranges of the tiles themselves (a few loads a warp);
+// beyond it they come from a launch of their own.
+constexpr int kOwnDocTiles = 32;
 
 // First distance of every bucket of one direction: buckets 0 .. n/2 - 1 hold one distance each, the rest grow
 // logarithmically up to `distance`, the last one holds everything beyond.
@@ -68,16 +71,60 @@ __device__ __forceinline__ int doc_at(const DenseDims& a, int b, int x, int len)
   if (x < 0 || x >= len) return -1;
   return a.docs ? __ldg(a.docs + (int64_t)b * a.Skv + x) : 0;
 }
+// The smallest and largest id of positions x0 .. x0 + n - 1 (dead ones count as -1), in every lane of a warp.
+__device__ __forceinline__ int2 warp_doc_range(const DenseDims& a, int b, int x0, int n, int len, int lane) {
+  int lo = INT32_MAX, hi = -1;
+  for (int i = lane; i < n; i += 32) {
+    const int id = max(doc_at(a, b, x0 + i, len), -1);
+    lo = min(lo, id);
+    hi = max(hi, id);
+  }
+  return make_int2(__reduce_min_sync(0xffffffffu, lo), __reduce_max_sync(0xffffffffu, hi));
+}
 // Whether two ranges of ids can have a common document, and whether both are one and the same document.
 __device__ __forceinline__ bool docs_meet(int2 p, int2 q) { return p.x <= q.y && q.x <= p.y && p.y >= 0 && q.y >= 0; }
 __device__ __forceinline__ bool docs_one(int2 p, int2 q) { return p.x == p.y && q.x == q.y && p.x == q.x && p.x >= 0; }
 
-// tanh from one exponential and one reciprocal: |error| <= about 2e-7, where the hardware's tanh has 5e-4 (times a cap
-// of 50: a score off by 0.02, more than the operands' own rounding gives).
+// tanh, |error| <= about 2e-7 both ways (the hardware's tanh has 5e-4: times a cap of 50 a score off by 0.02, more than
+// the operands' own rounding gives).  Where a thread's arguments are all within [-1, 1] (scores below the cap, nearly
+// always), an odd polynomial on pairs, x p(x^2) with p fitted to tanh(x) / x for the least |error| of tanh on [0, 1]
+// (weighted least squares, weights raised where the error was large): 9 packed FMAs a pair, against two exponentials and
+// two reciprocals, whose pipe the softmax itself fills.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float tanh_any(float x) {
+  return fmaf(-2.f, rcp_approx(1.f + ex2(x * (2.f * 1.4426950408889634f))), 1.f);
+}
+struct TanhPoly {  // f * tanh
+  uint64_t c[7];
+  __device__ __forceinline__ explicit TanhPoly(float f) {
+    const float k[7] = {0.999999693f, -0.333321293f, 0.133195837f, -0.053265835f, 0.0199732811f, -0.00595127819f,
+                        0.000963771153f};
+#pragma unroll
+    for (int i = 0; i < 7; ++i) c[i] = f2pack(k[i] * f, k[i] * f);
+  }
+  __device__ __forceinline__ uint64_t operator()(uint64_t x) const {
+    const uint64_t u = mul_f32x2(x, x);
+    uint64_t y = c[6];
+#pragma unroll
+    for (int i = 5; i >= 0; --i) y = fma_f32x2(y, u, c[i]);
+    return mul_f32x2(y, x);
+  }
+};
+// Largest magnitude of 32 values against m.
+__device__ __forceinline__ float absmax32(const float (&v)[32], float m) {
+  float a = m, b = 0.f, c = 0.f, d = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    a = fmax3(a, fabsf(v[i]), fabsf(v[i + 1]));
+    b = fmax3(b, fabsf(v[i + 2]), fabsf(v[i + 3]));
+    c = fmax3(c, fabsf(v[i + 4]), fabsf(v[i + 5]));
+    d = fmax3(d, fabsf(v[i + 6]), fabsf(v[i + 7]));
+  }
+  return fmaxf(fmaxf(a, b), fmaxf(c, d));
 }
 
 template <bool F16>
@@ -114,6 +161,46 @@ __device__ __forceinline__ void store8(uint16_t* o, uint16_t* low, const float* 
   if (low) st16(low, make_uint4(r[0], r[1], r[2], r[3]));
 }
 
+// Tensor-core instructions of a converged issuer warp: every lane runs the issuing code with the same values, so that
+// descriptors stay in uniform registers, and the one lane with `leader` set issues.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void umma_ss_by(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_by(uint32_t leader, uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+      "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader)
+      : "memory");
+}
+
+// Registers of a warpgroup (four warps), given back or taken from those the block was launched with.
+template <int N>
+__device__ __forceinline__ void set_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---- launches (each in the file it names) ----------------------------------------------------------------
 // A [B,H,S,d] tensor with unit feature stride.
 struct DenseTensor {
@@ -122,15 +209,15 @@ struct DenseTensor {
 };
 struct DenseFwdPlan {
   int pack;    // query heads of one key head that share a query tile (a divisor of G)
-  int tok;     // tokens of a 128-row query tile
+  int rep;     // copies of the queries in a tile: 4 where they take at most 32 rows, else 1
+  int tok;     // tokens of a query tile
   int ntile;   // query tiles per (batch, head group)
   int dual;    // one query tile per block, its keys in two interleaved streams
   int nsplit;  // blocks that share one query tile's keys
 };
 DenseFwdPlan dense_fwd_plan(const DenseDims& a);
-// dense_prep.cu: ids' range (min, max) of every key tile: kdoc [B][ceil(Skv / 128)]; with qdoc, of every 64-row
-// sub-tile of the queries too: qdoc [B][ceil(Sq / 64)].
-int launch_dense_doc_ranges(const DenseDims& a, int2* kdoc, int2* qdoc, cudaStream_t st);
+// dense_prep.cu: ids' range (min, max) of every key tile: kdoc [B][ceil(Skv / 128)].
+int launch_dense_doc_ranges(const DenseDims& a, int2* kdoc, cudaStream_t st);
 // dense_fwd.cu: low.p may be null; part_o / part_lse: nsplit > 1 only.
 int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTensor& q, const DenseTensor& k,
                      const DenseTensor& v, const DenseTensor& o, const DenseTensor& low, float* lse, const int2* kdoc,
@@ -153,10 +240,11 @@ int dense_bwd_shares(const DenseDims& a);
 int launch_dense_bwd(const DenseDims& a, const DenseTensor& q, const DenseTensor& k, const DenseTensor& v,
                      const DenseTensor& dout, const DenseTensor& dk, const DenseTensor& dv, const DenseBwdBuf& w,
                      cudaStream_t st);
-// dense_prep.cu: the rows' statistics, dqacc = 0 and (fp16) the largest norms; the bias by distance; the results.
-int launch_dense_bwd_rows(const DenseDims& a, const DenseTensor& o, const DenseTensor& low, const DenseTensor& dout,
-                          const DenseTensor& v, const float* lse, const DenseBwdBuf& w, cudaStream_t st);
-int launch_dense_bias(const DenseDims& a, const BucketStarts& bs, const DenseBwdBuf& w, cudaStream_t st);
+// dense_prep.cu: before the main kernel (the rows' statistics, dqacc = 0, fp16: the largest norms, the ids' ranges, the
+// bias by distance) and after it (the results' last sums and roundings).
+int launch_dense_bwd_prep(const DenseDims& a, const BucketStarts& bs, const DenseTensor& o, const DenseTensor& low,
+                          const DenseTensor& dout, const DenseTensor& v, const float* lse, const DenseBwdBuf& w,
+                          int2* kdoc, int2* qdoc, cudaStream_t st);
 int launch_dense_bwd_out(const DenseDims& a, const DenseTensor& dq, const DenseTensor& dk, const DenseTensor& dv,
                          void* dtable, const DenseBwdBuf& w, cudaStream_t st);
 // Device status word of the current device (api.cu).

@@ -175,7 +175,7 @@ int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_ten
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   cudaStream_t st = (cudaStream_t)stream;
   int2* kdoc = reinterpret_cast<int2*>(wsb + w.kdoc);
-  if (a.docs) LH_TRY(launch_dense_doc_ranges(a, kdoc, nullptr, st));
+  if (a.docs && (a.Skv + kKeyTile - 1) / kKeyTile > kOwnDocTiles) LH_TRY(launch_dense_doc_ranges(a, kdoc, st));
   return launch_dense_fwd(a, bs, tq, tk, tv, to, tl, lse, kdoc,
                           reinterpret_cast<float*>(wsb + w.part_o), reinterpret_cast<float*>(wsb + w.part_lse), st);
 }
@@ -211,9 +211,7 @@ int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_te
   buf.bucket = wsb + w.bucket;
   buf.range = reinterpret_cast<int2*>(wsb + w.range);
   buf.dtpart = reinterpret_cast<float*>(wsb + w.dtpart);
-  if (a.docs) LH_TRY(launch_dense_doc_ranges(a, kdoc, qdoc, st));
-  if (a.table) LH_TRY(launch_dense_bias(a, bs, buf, st));
-  LH_TRY(launch_dense_bwd_rows(a, to, tl, tdo, tv, lse, buf, st));
+  LH_TRY(launch_dense_bwd_prep(a, bs, to, tl, tdo, tv, lse, buf, kdoc, qdoc, st));
   LH_TRY(launch_dense_bwd(a, tq, tk, tv, tdo, tdk, tdv, buf, st));
   return launch_dense_bwd_out(a, tdq, tdk, tdv, dtable, buf, st);
 }

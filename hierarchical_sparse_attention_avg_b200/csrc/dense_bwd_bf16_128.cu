@@ -1,0 +1,8 @@
+// dense_bwd_bf16_128.cu — the dense stage's backward kernels for bf16 rows of 128 features.
+#include "dense_bwd.cuh"
+
+namespace lh {
+namespace bwd {
+template int launch<128, false>(const CUtensorMap (&)[6], const BwdArgs&, cudaStream_t);
+}  // namespace bwd
+}  // namespace lh

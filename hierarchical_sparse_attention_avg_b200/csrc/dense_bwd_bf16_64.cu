@@ -1,0 +1,8 @@
+// dense_bwd_bf16_64.cu — the dense stage's backward kernels for bf16 rows of 64 features.
+#include "dense_bwd.cuh"
+
+namespace lh {
+namespace bwd {
+template int launch<64, false>(const CUtensorMap (&)[6], const BwdArgs&, cudaStream_t);
+}  // namespace bwd
+}  // namespace lh

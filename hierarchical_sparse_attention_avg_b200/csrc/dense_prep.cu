@@ -7,50 +7,47 @@ namespace lh {
 
 namespace {
 
-// One warp per 64 positions: the smallest and largest id among them (a dead position counts as -1).  Key tiles take
-// two such halves.  Reads each id once; launch-bound.
-__global__ void doc_ranges_kernel(const DenseDims a, int2* __restrict__ kdoc, int2* __restrict__ qdoc, int nk, int nq) {
-  const int w = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, lane = threadIdx.x % 32, b = blockIdx.y;
-  if (w >= nk + nq) return;
+// The ids' range (min, max; a dead position counts as -1) of tile w: key tiles first, then 64-row query sub-tiles.  One
+// warp each.
+__device__ __forceinline__ void doc_range(const DenseDims& a, int b, int w, int lane, int nk, int2* kdoc, int2* qdoc,
+                                          int nq) {
   const int len = dense_len(a, b);
   const bool key = w < nk;
   const int x0 = key ? w * kKeyTile : len - a.Sq + (w - nk) * 64;
   const int n = key ? min(kKeyTile, a.Skv - x0) : min(64, a.Sq - (w - nk) * 64);
-  int lo = INT32_MAX, hi = -1;
-  for (int i = lane; i < n; i += 32) {
-    const int id = max(doc_at(a, b, x0 + i, len), -1);
-    lo = min(lo, id);
-    hi = max(hi, id);
-  }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) (key ? kdoc[(int64_t)b * nk + w] : qdoc[(int64_t)b * nq + w - nk]) = make_int2(lo, hi);
+  const int2 r = warp_doc_range(a, b, x0, n, len, lane);
+  if (lane == 0) (key ? kdoc[(int64_t)b * nk + w] : qdoc[(int64_t)b * nq + w - nk]) = r;
+}
+
+__global__ void __launch_bounds__(256) doc_ranges_kernel(const DenseDims a, int2* __restrict__ kdoc, int nk) {
+  const int w = blockIdx.x * 8 + threadIdx.x / 32;
+  if (w < nk) doc_range(a, blockIdx.y, w, threadIdx.x % 32, nk, kdoc, nullptr, 0);
 }
 
 // One group of d / 8 lanes per query row, 16-byte loads: D = <dO, O>, the statistics, the zeroed dQ accumulator, and for
 // fp16 the largest |dO_i| of the key head's rows (one atomicMax of a bit pattern per block: order-free).
 template <int D, bool F16>
-__global__ void __launch_bounds__(256)
-    bwd_rows_kernel(const DenseDims a, const uint16_t* __restrict__ o, Strides os, const uint16_t* __restrict__ low,
-                    Strides ls, const uint16_t* __restrict__ dout, Strides ds, const float* __restrict__ lse, float* __restrict__ stats, float* __restrict__ dqacc,
-                    unsigned int* __restrict__ amax) {
+__device__ __forceinline__ void bwd_row(const DenseDims& a, const DenseTensor& o, const DenseTensor& low,
+                                        const DenseTensor& dout, const float* __restrict__ lse, const DenseBwdBuf& w,
+                                        int blk, int bh) {
   constexpr int L = D / 8, ROWS = 256 / L;
-  const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq;
-  const int i = blockIdx.x * ROWS + threadIdx.x / L, f = (threadIdx.x % L) * 8;
+  const int b = bh / a.Hq, h = bh % a.Hq;
+  const int i = blk * ROWS + threadIdx.x / L, f = (threadIdx.x % L) * 8;
   const bool in = i < a.Sq;
+  auto at = [&](const DenseTensor& t) {
+    return ld16(static_cast<const uint16_t*>(t.p) + b * t.st.b + h * t.st.h + (int64_t)i * t.st.s + f);
+  };
   float dot = 0.f, norm = 0.f;
   if (in) {
-    const uint4 x = ld16(o + b * os.b + h * os.h + (int64_t)i * os.s + f);
-    const uint4 y = ld16(dout + b * ds.b + h * ds.h + (int64_t)i * ds.s + f);
-    const uint4 z = low ? ld16(low + b * ls.b + h * ls.h + (int64_t)i * ls.s + f) : make_uint4(0, 0, 0, 0);
+    const uint4 x = at(o), y = at(dout), z = low.p ? at(low) : make_uint4(0, 0, 0, 0);
     const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w}, zw[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 u = unpack2<F16>(xw[e]), w = unpack2<F16>(yw[e]), r = unpack2<F16>(zw[e]);
-      dot = fmaf(u.x + r.x, w.x, fmaf(u.y + r.y, w.y, dot));
-      norm = fmaf(w.x, w.x, fmaf(w.y, w.y, norm));
+      const float2 u = unpack2<F16>(xw[e]), v = unpack2<F16>(yw[e]), r = unpack2<F16>(zw[e]);
+      dot = fmaf(u.x + r.x, v.x, fmaf(u.y + r.y, v.y, dot));
+      norm = fmaf(v.x, v.x, fmaf(v.y, v.y, norm));
     }
-    float4* acc = reinterpret_cast<float4*>(dqacc + ((int64_t)bh * a.Sq + i) * D + f);
+    float4* acc = reinterpret_cast<float4*>(w.dqacc + ((int64_t)bh * a.Sq + i) * D + f);
     acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 #pragma unroll
@@ -65,8 +62,8 @@ __global__ void __launch_bounds__(256)
     dead = l == -INFINITY || doc_at(a, b, len - a.Sq + i, len) < 0;
     if (f == 0) {
       const int64_t pitch = (a.Sq + 3) & ~3, at = bh * pitch + i;
-      stats[at] = dead ? -INFINITY : fmaf(l, -1.4426950408889634f, F16 ? 12.f : 0.f);
-      stats[(int64_t)a.B * a.Hq * pitch + at] = dead ? 0.f : -dot;
+      w.stats[at] = dead ? -INFINITY : fmaf(l, -1.4426950408889634f, F16 ? 12.f : 0.f);
+      w.stats[(int64_t)a.B * a.Hq * pitch + at] = dead ? 0.f : -dot;
     }
   }
   if (F16) {
@@ -75,31 +72,31 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     if (!dead && f == 0) atomicMax(&s_max, __float_as_uint(sqrtf(norm)));
     __syncthreads();
-    if (threadIdx.x == 0) atomicMax(amax + 2 * (b * a.Hkv + h / a.G), s_max);
+    if (threadIdx.x == 0) atomicMax(w.amax + 2 * (b * a.Hkv + h / a.G), s_max);
   }
 }
 
 // fp16: the largest |V_j| of a key head.
 template <int D>
-__global__ void __launch_bounds__(256) v_norm_kernel(const DenseDims a, const uint16_t* __restrict__ v, Strides vs,
-                                                     unsigned int* __restrict__ amax) {
+__device__ __forceinline__ void v_norm(const DenseDims& a, const DenseTensor& v, unsigned int* __restrict__ amax, int blk,
+                                       int bh) {
   constexpr int L = D / 8, ROWS = 256 / L;
-  const int bh = blockIdx.y, b = bh / a.Hkv, h = bh % a.Hkv, len = dense_len(a, b);
+  const int b = bh / a.Hkv, h = bh % a.Hkv, len = dense_len(a, b);
   const int f = (threadIdx.x % L) * 8;
   __shared__ unsigned int s_max;
   if (threadIdx.x == 0) s_max = 0;
   __syncthreads();
   for (int k = 0; k < 8; ++k) {
-    const int j = (blockIdx.x * 8 + k) * ROWS + threadIdx.x / L;
+    const int j = (blk * 8 + k) * ROWS + threadIdx.x / L;
     float norm = 0.f;
     const bool live = j < len && doc_at(a, b, j, len) >= 0;
     if (live) {
-      const uint4 y = ld16(v + b * vs.b + h * vs.h + (int64_t)j * vs.s + f);
+      const uint4 y = ld16(static_cast<const uint16_t*>(v.p) + b * v.st.b + h * v.st.h + (int64_t)j * v.st.s + f);
       const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 w = unpack2<true>(yw[e]);
-        norm = fmaf(w.x, w.x, fmaf(w.y, w.y, norm));
+        const float2 u = unpack2<true>(yw[e]);
+        norm = fmaf(u.x, u.x, fmaf(u.y, u.y, norm));
       }
     }
 #pragma unroll
@@ -110,32 +107,61 @@ __global__ void __launch_bounds__(256) v_norm_kernel(const DenseDims a, const ui
   if (threadIdx.x == 0) atomicMax(amax + 2 * bh + 1, s_max);
 }
 
-// The bias by distance, for every head; block row 0 also writes the buckets by distance and their ranges.
+// The bias by distance of head h; head 0 also writes the buckets by distance and their ranges.
 template <bool F16>
-__global__ void bias_kernel(const DenseDims a, const __grid_constant__ BucketStarts bs, float* __restrict__ bias,
-                            uint8_t* __restrict__ bucket, int2* __restrict__ range) {
-  const int wide = 2 * a.near + 1, h = blockIdx.y;
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < wide; i += gridDim.x * blockDim.x) {
+__device__ __forceinline__ void bias_by_distance(const DenseDims& a, const BucketStarts& bs, const DenseBwdBuf& w, int blk,
+                                                 int h) {
+  const int wide = 2 * a.near + 1, i = blk * 256 + threadIdx.x;
+  if (i < wide) {
     const int k = bucket_of(bs, i - a.near);
-    bias[(int64_t)h * wide + i] = 1.4426950408889634f * table_at<F16>(a.table, (int64_t)h * a.buckets + k);
-    if (h == 0) bucket[i] = (uint8_t)k;
+    w.bias[(int64_t)h * wide + i] = 1.4426950408889634f * table_at<F16>(a.table, (int64_t)h * a.buckets + k);
+    if (h == 0) w.bucket[i] = (uint8_t)k;
   }
   const int k = threadIdx.x;
-  if (h == 0 && blockIdx.x == 0 && k < a.buckets) {
+  if (h == 0 && blk == 0 && k < a.buckets) {
     const int m = k % bs.n;
     const int lo = bs.start[m], hi = m + 1 < bs.n ? bs.start[m + 1] - 1 : 1 << 29;  // sizes lo .. hi
     int2 r;
     if (!bs.both) r = make_int2(m == 0 ? -(1 << 29) : lo, hi);
     else r = k < bs.n ? make_int2(lo, hi) : make_int2(-hi, min(-lo, -1));
-    range[k] = r;
+    w.range[k] = r;
+  }
+}
+
+// Everything the backward needs before its main kernel, in one launch: blocks [0, e0) row statistics, [e0, e1) value
+// norms, [e1, e2) ids' ranges, [e2, end) bias.
+struct PrepArgs {
+  DenseDims a;
+  BucketStarts bs;
+  DenseTensor o, low, dout, v;
+  const float* lse;
+  DenseBwdBuf w;
+  int2 *kdoc, *qdoc;
+  int row_blocks, v_blocks, doc_blocks, bias_blocks;  // per head, head, batch entry, head
+  int64_t e0, e1, e2;
+};
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ PrepArgs p) {
+  const int64_t x = blockIdx.x;
+  if (x < p.e0) {
+    bwd_row<D, F16>(p.a, p.o, p.low, p.dout, p.lse, p.w, (int)(x % p.row_blocks), (int)(x / p.row_blocks));
+  } else if (x < p.e1) {
+    if (F16) v_norm<D>(p.a, p.v, p.w.amax, (int)((x - p.e0) % p.v_blocks), (int)((x - p.e0) / p.v_blocks));
+  } else if (x < p.e2) {
+    const int nk = (p.a.Skv + kKeyTile - 1) / kKeyTile, nq = (p.a.Sq + 63) / 64;
+    const int w = (int)((x - p.e1) % p.doc_blocks) * 8 + threadIdx.x / 32;
+    if (w < nk + nq)
+      doc_range(p.a, (int)((x - p.e1) / p.doc_blocks), w, threadIdx.x % 32, nk, p.kdoc, p.qdoc, nq);
+  } else {
+    bias_by_distance<F16>(p.a, p.bs, p.w, (int)((x - p.e2) % p.bias_blocks), (int)((x - p.e2) / p.bias_blocks));
   }
 }
 
 // dQ: the accumulator rounded once; dV, dK: the shares' sums rounded once.  Eight features a thread.
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) bwd_out_kernel(const float* __restrict__ src, int64_t plane, int n, int heads,
-                                                      int rows, void* __restrict__ out, Strides st, int64_t total) {
-  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+__device__ __forceinline__ void round_rows(const float* __restrict__ src, int64_t plane, int n, int heads, int rows,
+                                           const DenseTensor& out, int64_t total, int64_t blk) {
+  const int64_t e = (blk * 256 + threadIdx.x) * 8;
   if (e >= total) return;
   float v[8] = {};
   for (int s = 0; s < n; ++s) {
@@ -145,7 +171,8 @@ __global__ void __launch_bounds__(256) bwd_out_kernel(const float* __restrict__ 
     v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
   }
   const int64_t row = e / D, i = row % rows, bh = row / rows;
-  uint16_t* dst = static_cast<uint16_t*>(out) + (bh / heads) * st.b + (bh % heads) * st.h + i * st.s + e % D;
+  uint16_t* dst = static_cast<uint16_t*>(const_cast<void*>(out.p)) + (bh / heads) * out.st.b + (bh % heads) * out.st.h +
+                  i * out.st.s + e % D;
   st16(dst, make_uint4(pack2_rn<F16>(v[0], v[1]), pack2_rn<F16>(v[2], v[3]), pack2_rn<F16>(v[4], v[5]),
                        pack2_rn<F16>(v[6], v[7])));
 }
@@ -153,15 +180,17 @@ __global__ void __launch_bounds__(256) bwd_out_kernel(const float* __restrict__ 
 // dtable[h][k]: the warps' sums of every batch entry and key tile, in a fixed order; 64-bit, as a far bucket's sum is the
 // small rest of large ones.
 template <bool F16>
-__global__ void __launch_bounds__(256) dtable_kernel(const DenseDims a, const float* __restrict__ part, int nkt,
-                                                     void* __restrict__ dtable) {
-  const int h = blockIdx.x, kvh = h / a.G, g = h % a.G, k = blockIdx.y * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
+__device__ __forceinline__ void dtable_rows(const DenseDims& a, const float* __restrict__ part, int nkt, void* dtable,
+                                            int h, int k0) {
+  const int kvh = h / a.G, g = h % a.G, k = k0 + threadIdx.x % 32, w = threadIdx.x / 32;
   __shared__ double s_sum[8][32];
   double sum = 0.0;
   if (k < a.buckets)
-    for (int64_t t = 0; t < (int64_t)a.B * nkt; ++t) {
-      const int64_t b = t / nkt, kt = t % nkt;
-      sum += part[((((b * a.Hkv + kvh) * nkt + kt) * a.G + g) * 8 + w) * a.buckets + k];
+    for (int b = 0; b < a.B; ++b) {
+      const float* src = part + ((((int64_t)b * a.Hkv + kvh) * nkt * a.G + g) * 8 + w) * a.buckets + k;
+      const int64_t step = (int64_t)a.G * 8 * a.buckets;
+#pragma unroll 8
+      for (int kt = 0; kt < nkt; ++kt) sum += src[kt * step];
     }
   s_sum[w][threadIdx.x % 32] = sum;
   __syncthreads();
@@ -171,72 +200,80 @@ __global__ void __launch_bounds__(256) dtable_kernel(const DenseDims a, const fl
   }
 }
 
+// The results, in one launch: blocks [0, e0) dtable (the longest first), [e0, e1) dQ, then, with shared query heads,
+// dV and dK.
+struct OutArgs {
+  DenseDims a;
+  DenseTensor dq, dk, dv;
+  void* dtable;
+  DenseBwdBuf w;
+  int nkt, shares;
+  int64_t e0, e1, kv_blocks;
+};
 template <int D, bool F16>
-int rows_t(const DenseDims& a, const DenseTensor& o, const DenseTensor& low, const DenseTensor& dout, const DenseTensor& v, const float* lse,
-           const DenseBwdBuf& w, cudaStream_t st) {
-  constexpr int ROWS = 256 / (D / 8);
-  KernelTimer timer("dense_bwd_rows", st);
-  if (F16 && cudaMemsetAsync(w.amax, 0, (size_t)a.B * a.Hkv * 8, st) != cudaSuccess) return LH_ERR_CUDA;
-  bwd_rows_kernel<D, F16><<<dim3((a.Sq + ROWS - 1) / ROWS, a.B * a.Hq), 256, 0, st>>>(
-      a, static_cast<const uint16_t*>(o.p), o.st, static_cast<const uint16_t*>(low.p), low.st,
-      static_cast<const uint16_t*>(dout.p), dout.st, lse, w.stats, w.dqacc,
-      w.amax);
-  if (F16)
-    v_norm_kernel<D><<<dim3((a.Skv + 8 * ROWS - 1) / (8 * ROWS), a.B * a.Hkv), 256, 0, st>>>(
-        a, static_cast<const uint16_t*>(v.p), v.st, w.amax);
-  return check_launch();
-}
-
-template <int D, bool F16>
-int out_t(const DenseDims& a, const DenseTensor& dq, const DenseTensor& dk, const DenseTensor& dv, void* dtable,
-          const DenseBwdBuf& w, cudaStream_t st) {
-  KernelTimer timer("dense_bwd_out", st);
-  auto run = [&](const float* src, int64_t plane, int n, int heads, int rows, const DenseTensor& t) {
-    const int64_t total = (int64_t)a.B * heads * rows * D;
-    bwd_out_kernel<D, F16><<<(unsigned)((total / 8 + 255) / 256), 256, 0, st>>>(src, plane, n, heads, rows,
-                                                                               const_cast<void*>(t.p), t.st, total);
-  };
-  run(w.dqacc, 0, 1, a.Hq, a.Sq, dq);
-  const int shares = dense_bwd_shares(a);
-  if (shares > 1) {
-    const int64_t one = (int64_t)a.B * a.Hkv * a.Skv * D;
-    run(w.dkv, 2 * one, shares, a.Hkv, a.Skv, dv);
-    run(w.dkv + one, 2 * one, shares, a.Hkv, a.Skv, dk);
+__global__ void __launch_bounds__(256) bwd_out_kernel(const __grid_constant__ OutArgs p) {
+  const DenseDims& a = p.a;
+  const int64_t x = blockIdx.x, one = (int64_t)a.B * a.Hkv * a.Skv * D;
+  if (x < p.e0) {
+    const int n = (a.buckets + 31) / 32;
+    dtable_rows<F16>(a, p.w.dtpart, p.nkt, p.dtable, (int)(x / n), (int)(x % n) * 32);
+  } else if (x < p.e1) {
+    round_rows<D, F16>(p.w.dqacc, 0, 1, a.Hq, a.Sq, p.dq, (int64_t)a.B * a.Hq * a.Sq * D, x - p.e0);
+  } else if (x < p.e1 + p.kv_blocks) {
+    round_rows<D, F16>(p.w.dkv, 2 * one, p.shares, a.Hkv, a.Skv, p.dv, one, x - p.e1);
+  } else {
+    round_rows<D, F16>(p.w.dkv + one, 2 * one, p.shares, a.Hkv, a.Skv, p.dk, one, x - p.e1 - p.kv_blocks);
   }
-  if (a.table)
-    dtable_kernel<F16><<<dim3(a.Hq, (a.buckets + 31) / 32), 256, 0, st>>>(a, w.dtpart, (a.Skv + kKeyTile - 1) / kKeyTile,
-                                                                         dtable);
-  return check_launch();
 }
 
 }  // namespace
 
-int launch_dense_bwd_rows(const DenseDims& a, const DenseTensor& o, const DenseTensor& low, const DenseTensor& dout,
-                          const DenseTensor& v, const float* lse, const DenseBwdBuf& w, cudaStream_t st) {
-  auto run = a.d == 64 ? (a.f16 ? rows_t<64, true> : rows_t<64, false>) : (a.f16 ? rows_t<128, true> : rows_t<128, false>);
-  return run(a, o, low, dout, v, lse, w, st);
-}
-
-int launch_dense_bias(const DenseDims& a, const BucketStarts& bs, const DenseBwdBuf& w, cudaStream_t st) {
-  KernelTimer timer("dense_bias", st);
-  const int blocks = (2 * a.near + 1 + 255) / 256;
-  const dim3 grid(blocks < 64 ? blocks : 64, a.Hq);
-  if (a.f16) bias_kernel<true><<<grid, 256, 0, st>>>(a, bs, w.bias, w.bucket, w.range);
-  else bias_kernel<false><<<grid, 256, 0, st>>>(a, bs, w.bias, w.bucket, w.range);
+int launch_dense_bwd_prep(const DenseDims& a, const BucketStarts& bs, const DenseTensor& o, const DenseTensor& low,
+                          const DenseTensor& dout, const DenseTensor& v, const float* lse, const DenseBwdBuf& w,
+                          int2* kdoc, int2* qdoc, cudaStream_t st) {
+  PrepArgs p;
+  p.a = a; p.bs = bs; p.o = o; p.low = low; p.dout = dout; p.v = v; p.lse = lse; p.w = w; p.kdoc = kdoc; p.qdoc = qdoc;
+  const int rows = 256 / (a.d / 8), nk = (a.Skv + kKeyTile - 1) / kKeyTile, nq = (a.Sq + 63) / 64;
+  p.row_blocks = (a.Sq + rows - 1) / rows;
+  p.v_blocks = a.f16 ? (a.Skv + 8 * rows - 1) / (8 * rows) : 0;
+  p.doc_blocks = a.docs ? (nk + nq + 7) / 8 : 0;
+  p.bias_blocks = a.table ? (2 * a.near + 1 + 255) / 256 : 0;
+  p.e0 = (int64_t)p.row_blocks * a.B * a.Hq;
+  p.e1 = p.e0 + (int64_t)p.v_blocks * a.B * a.Hkv;
+  p.e2 = p.e1 + (int64_t)p.doc_blocks * a.B;
+  const int64_t blocks = p.e2 + (int64_t)p.bias_blocks * a.Hq;
+  if (blocks > INT32_MAX) return LH_ERR_UNSUPPORTED;
+  KernelTimer timer("dense_bwd_prep", st);
+  if (a.f16 && cudaMemsetAsync(w.amax, 0, (size_t)a.B * a.Hkv * 8, st) != cudaSuccess) return LH_ERR_CUDA;
+  auto kernel = a.d == 64 ? (a.f16 ? bwd_prep_kernel<64, true> : bwd_prep_kernel<64, false>)
+                          : (a.f16 ? bwd_prep_kernel<128, true> : bwd_prep_kernel<128, false>);
+  kernel<<<(unsigned)blocks, 256, 0, st>>>(p);
   return check_launch();
 }
 
 int launch_dense_bwd_out(const DenseDims& a, const DenseTensor& dq, const DenseTensor& dk, const DenseTensor& dv,
                          void* dtable, const DenseBwdBuf& w, cudaStream_t st) {
-  return a.d == 64 ? (a.f16 ? out_t<64, true>(a, dq, dk, dv, dtable, w, st) : out_t<64, false>(a, dq, dk, dv, dtable, w, st))
-                   : (a.f16 ? out_t<128, true>(a, dq, dk, dv, dtable, w, st)
-                            : out_t<128, false>(a, dq, dk, dv, dtable, w, st));
+  OutArgs p;
+  p.a = a; p.dq = dq; p.dk = dk; p.dv = dv; p.dtable = dtable; p.w = w;
+  p.nkt = (a.Skv + kKeyTile - 1) / kKeyTile;
+  p.shares = dense_bwd_shares(a);
+  auto blocks_of = [&](int64_t rows) { return (rows * (a.d / 8) + 255) / 256; };
+  p.e0 = a.table ? (int64_t)a.Hq * ((a.buckets + 31) / 32) : 0;
+  p.e1 = p.e0 + blocks_of((int64_t)a.B * a.Hq * a.Sq);
+  p.kv_blocks = p.shares > 1 ? blocks_of((int64_t)a.B * a.Hkv * a.Skv) : 0;
+  const int64_t blocks = p.e1 + 2 * p.kv_blocks;
+  if (blocks > INT32_MAX) return LH_ERR_UNSUPPORTED;
+  KernelTimer timer("dense_bwd_out", st);
+  auto kernel = a.d == 64 ? (a.f16 ? bwd_out_kernel<64, true> : bwd_out_kernel<64, false>)
+                          : (a.f16 ? bwd_out_kernel<128, true> : bwd_out_kernel<128, false>);
+  kernel<<<(unsigned)blocks, 256, 0, st>>>(p);
+  return check_launch();
 }
 
-int launch_dense_doc_ranges(const DenseDims& a, int2* kdoc, int2* qdoc, cudaStream_t st) {
-  const int nk = (a.Skv + kKeyTile - 1) / kKeyTile, nq = qdoc ? (a.Sq + 63) / 64 : 0;
+int launch_dense_doc_ranges(const DenseDims& a, int2* kdoc, cudaStream_t st) {
+  const int nk = (a.Skv + kKeyTile - 1) / kKeyTile;
   KernelTimer timer("dense_doc_ranges", st);
-  doc_ranges_kernel<<<dim3((nk + nq + 7) / 8, a.B), 256, 0, st>>>(a, kdoc, qdoc, nk, nq);
+  doc_ranges_kernel<<<dim3((nk + 7) / 8, a.B), 256, 0, st>>>(a, kdoc, nk);
   return check_launch();
 }
 

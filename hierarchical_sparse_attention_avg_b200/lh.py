@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -47,14 +48,6 @@ class LhAttnParams(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "Sq", "Skv", "d", "dtype", "causal")] +
                 [(n, ctypes.c_float) for n in ("scale", "softcap")] +
                 [(n, ctypes.c_int32) for n in ("buckets", "max_distance", "bidirectional")])
-
-
-class LhTensor(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("stride_b", "stride_h", "stride_s")]
-
-
-class LhAttnMods(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("slopes", "table", "docs", "prefix", "kv_len")]
 
 
 class LighthouseError(RuntimeError):
@@ -516,6 +509,8 @@ class AttnParams:
         object.__setattr__(self, "_c", c)  # read by every call, built once
         object.__setattr__(self, "_ref", ctypes.addressof(c))
         object.__setattr__(self, "_status", _lib.lh_attn_validate(self._ref))
+        object.__setattr__(self, "_qs", (self.B, self.Hq, self.Sq, self.d))
+        object.__setattr__(self, "_ks", (self.B, self.Hkv, self.Skv, self.d))
 
     def c(self) -> LhAttnParams:
         return self._c
@@ -544,29 +539,35 @@ def lh_attn_bucket_starts(P: AttnParams) -> list:
     return list(buf[:n])
 
 
-def _rows(t, shape, dtype, device, name) -> LhTensor:
+_pack_rows = struct.Struct("4q").pack  # an lh_tensor
+_pack_mods = struct.Struct("5Q").pack  # an lh_attn_mods
+
+
+def _rows(t, shape, dtype, device, name) -> bytes:
     """Descriptor of a [B, H, S, d] tensor with any layout the library takes: unit feature stride, the others multiples
     of 8 elements."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     sb, sh, ss, sd = t.stride()
-    B, H, S, d = shape
-    if sd != 1 or (B > 1 and (sb <= 0 or sb & 7)) or (H > 1 and (sh <= 0 or sh & 7)) or (S > 1 and (ss <= 0 or ss & 7)):
-        raise ValueError(f"{name}: features must be contiguous and the other strides positive multiples of 8, got {t.stride()}")
-    return LhTensor(t.data_ptr(), sb, sh, ss)
+    if sd != 1 or sb & 7 or sh & 7 or ss & 7 or sb <= 0 or sh <= 0 or ss <= 0:
+        B, H, S, d = shape  # (a dimension of one may have any stride)
+        if (sd != 1 and d > 1) or any(n > 1 and (x <= 0 or x & 7) for n, x in ((B, sb), (H, sh), (S, ss))):
+            raise ValueError(f"{name}: features must be contiguous and the other strides positive multiples of 8, got "
+                             f"{t.stride()}")
+    return _pack_rows(t.data_ptr(), sb, sh, ss)
 
 
-def _vec(t, shape, dtype, device, name):
+def _vec(t, shape, dtype, device, name) -> int:
     if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _attn_mods(P: AttnParams, dev, slopes, table, docs, prefix, kv_len) -> LhAttnMods:
-    return LhAttnMods(_vec(slopes, (P.Hq,), torch.float32, dev, "slopes"),
+def _attn_mods(P: AttnParams, dev, slopes, table, docs, prefix, kv_len) -> bytes:
+    return _pack_mods(_vec(slopes, (P.Hq,), torch.float32, dev, "slopes"),
                       _vec(table, (P.Hq, P.buckets), P.dtype, dev, "table"),
                       _vec(docs, (P.B, P.Skv), torch.int32, dev, "docs"),
                       _vec(prefix, (P.B,), torch.int32, dev, "prefix"),
@@ -583,13 +584,16 @@ def _attn_ws(P: AttnParams, ws, dev, backward, where):
     return ws
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on_device(dev, fn, *args) -> int:
     """The call with the tensors' device current, on its current stream."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
     if dev.index == torch.cuda.current_device():
-        return fn(*args, stream)
+        return fn(*args, _raw_stream(dev.index))
     with torch.cuda.device(dev):
-        return fn(*args, stream)
+        return fn(*args, _raw_stream(dev.index))
 
 
 def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, prefix=None, kv_len=None, o=None,
@@ -601,16 +605,15 @@ def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, 
     _check(P._status, "lh_attn_forward")
     dev = q.device
     ws = _attn_ws(P, ws, dev, False, "lh_attn_forward")
-    qs, ks = (P.B, P.Hq, P.Sq, P.d), (P.B, P.Hkv, P.Skv, P.d)
+    qs, ks = P._qs, P._ks
     if o is None:
         o = torch.empty(qs, dtype=P.dtype, device=dev)
     if lse is None:
         lse = torch.empty(qs[:3], dtype=torch.float32, device=dev)
-    mods = _attn_mods(P, dev, slopes, table, docs, prefix, kv_len)
-    rc = _on_device(dev, _lib.lh_attn_forward, P._ref, ctypes.byref(mods),
-                    ctypes.byref(_rows(q, qs, P.dtype, dev, "q")), ctypes.byref(_rows(k, ks, P.dtype, dev, "k")),
-                    ctypes.byref(_rows(v, ks, P.dtype, dev, "v")), ctypes.byref(_rows(o, qs, P.dtype, dev, "o")),
-                    None if low is None else ctypes.byref(_rows(low, qs, P.dtype, dev, "low")),
+    dt = P.dtype
+    rc = _on_device(dev, _lib.lh_attn_forward, P._ref, _attn_mods(P, dev, slopes, table, docs, prefix, kv_len),
+                    _rows(q, qs, dt, dev, "q"), _rows(k, ks, dt, dev, "k"), _rows(v, ks, dt, dev, "v"),
+                    _rows(o, qs, dt, dev, "o"), None if low is None else _rows(low, qs, dt, dev, "low"),
                     _vec(lse, qs[:3], torch.float32, dev, "lse"), ws.data_ptr(), ws.numel())
     _check(rc, "lh_attn_forward")
     return o, lse
@@ -623,18 +626,18 @@ def lh_attn_backward(P: AttnParams, q, k, v, o, lse, dout, slopes=None, table=No
     _check(P._status, "lh_attn_backward")
     dev = q.device
     ws = _attn_ws(P, ws, dev, True, "lh_attn_backward")
-    qs, ks = (P.B, P.Hq, P.Sq, P.d), (P.B, P.Hkv, P.Skv, P.d)
+    qs, ks = P._qs, P._ks
     dq = torch.empty(qs, dtype=P.dtype, device=dev) if dq is None else dq
     dk = torch.empty(ks, dtype=P.dtype, device=dev) if dk is None else dk
     dv = torch.empty(ks, dtype=P.dtype, device=dev) if dv is None else dv
     if P.buckets and dtable is None:
         dtable = torch.empty((P.Hq, P.buckets), dtype=P.dtype, device=dev)
-    mods = _attn_mods(P, dev, slopes, table, docs, prefix, kv_len)
-    t = [ctypes.byref(_rows(x, s, P.dtype, dev, n)) for x, s, n in
-         ((q, qs, "q"), (k, ks, "k"), (v, ks, "v"), (o, qs, "o"), (dout, qs, "dout"), (dq, qs, "dq"), (dk, ks, "dk"),
-          (dv, ks, "dv"))]
-    rc = _on_device(dev, _lib.lh_attn_backward, P._ref, ctypes.byref(mods), t[0], t[1], t[2], t[3],
-                    None if low is None else ctypes.byref(_rows(low, qs, P.dtype, dev, "low")), _vec(lse, qs[:3], torch.float32, dev, "lse"), t[4], t[5], t[6], t[7],
-                    _vec(dtable, (P.Hq, P.buckets), P.dtype, dev, "dtable"), ws.data_ptr(), ws.numel())
+    dt = P.dtype
+    rc = _on_device(dev, _lib.lh_attn_backward, P._ref, _attn_mods(P, dev, slopes, table, docs, prefix, kv_len),
+                    _rows(q, qs, dt, dev, "q"), _rows(k, ks, dt, dev, "k"), _rows(v, ks, dt, dev, "v"),
+                    _rows(o, qs, dt, dev, "o"), None if low is None else _rows(low, qs, dt, dev, "low"),
+                    _vec(lse, qs[:3], torch.float32, dev, "lse"), _rows(dout, qs, dt, dev, "dout"),
+                    _rows(dq, qs, dt, dev, "dq"), _rows(dk, ks, dt, dev, "dk"), _rows(dv, ks, dt, dev, "dv"),
+                    _vec(dtable, (P.Hq, P.buckets), dt, dev, "dtable"), ws.data_ptr(), ws.numel())
     _check(rc, "lh_attn_backward")
     return dq, dk, dv, dtable
