@@ -71,19 +71,38 @@ __device__ __forceinline__ int doc_at(const DenseDims& a, int b, int x, int len)
   if (x < 0 || x >= len) return -1;
   return a.docs ? __ldg(a.docs + (int64_t)b * a.Skv + x) : 0;
 }
-// The smallest and largest id of positions x0 .. x0 + n - 1 (dead ones count as -1), in every lane of a warp.
+// Ids of a run of positions: x the smallest and y the largest (-1: none) among its live ones; x is complemented (and so
+// negative) where some position is dead.
+__device__ __forceinline__ int2 id_range(int lo, int hi, bool dead) { return make_int2(dead ? ~lo : lo, hi); }
+// That of positions x0 .. x0 + n - 1, in every lane of a warp.
 __device__ __forceinline__ int2 warp_doc_range(const DenseDims& a, int b, int x0, int n, int len, int lane) {
   int lo = INT32_MAX, hi = -1;
+  bool dead = false;
   for (int i = lane; i < n; i += 32) {
-    const int id = max(doc_at(a, b, x0 + i, len), -1);
-    lo = min(lo, id);
-    hi = max(hi, id);
+    const int id = doc_at(a, b, x0 + i, len);
+    if (id < 0) dead = true;
+    else lo = min(lo, id), hi = max(hi, id);
   }
-  return make_int2(__reduce_min_sync(0xffffffffu, lo), __reduce_max_sync(0xffffffffu, hi));
+  return id_range(__reduce_min_sync(0xffffffffu, lo), __reduce_max_sync(0xffffffffu, hi),
+                  __any_sync(0xffffffffu, dead));
 }
-// Whether two ranges of ids can have a common document, and whether both are one and the same document.
-__device__ __forceinline__ bool docs_meet(int2 p, int2 q) { return p.x <= q.y && q.x <= p.y && p.y >= 0 && q.y >= 0; }
-__device__ __forceinline__ bool docs_one(int2 p, int2 q) { return p.x == p.y && q.x == q.y && p.x == q.x && p.x >= 0; }
+// Whether two runs can have a common document, and whether both are wholly of one and the same document.
+__device__ __forceinline__ bool docs_meet(int2 p, int2 q) {
+  return (p.x < 0 ? ~p.x : p.x) <= q.y && (q.x < 0 ? ~q.x : q.x) <= p.y;
+}
+__device__ __forceinline__ bool docs_one(int2 p, int2 q) { return p.x == p.y && q.x == q.y && p.x == q.x; }
+// Bit i: position of lane i has this lane's document (`other` and `mine`: their ids; one document after the other).
+__device__ __forceinline__ uint32_t same_doc(int other, int mine) {
+  uint32_t todo = __ballot_sync(0xffffffffu, mine >= 0), same = 0;
+#pragma unroll 1
+  while (todo) {
+    const int doc = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
+    const uint32_t m = __ballot_sync(0xffffffffu, other == doc);
+    if (mine == doc) same = m;
+    todo &= ~__ballot_sync(0xffffffffu, mine == doc);
+  }
+  return same;
+}
 
 // tanh, |error| <= about 2e-7 both ways (the hardware's tanh has 5e-4: times a cap of 50 a score off by 0.02, more than
 // the operands' own rounding gives).  Where a thread's arguments are all within [-1, 1] (scores below the cap, nearly

@@ -309,12 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole) {
           const int lo = max(max(key < prefix || !a.causal ? 0 : key - x0, -x0), 0), hi = min(a.Sq - row0, 32);
           vis = kdead || lo >= hi ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);  // rows [lo, hi)
-          if (a.docs) {
-            uint32_t same = 0;
-#pragma unroll 8
-            for (int c = 0; c < 32; ++c) same |= (uint32_t)(doc_at(a, b, x0 + c, len) == kid) << c;
-            vis &= same;
-          }
+          if (a.docs) vis &= same_doc(doc_at(a, b, x0 + lane, len), kid);
         }
         uint32_t pk[16], dk[16];
         const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * Lay::ST) + 8 * hc;

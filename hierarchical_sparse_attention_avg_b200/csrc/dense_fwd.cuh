@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ WaitCtl s_wait;
   __shared__ BucketStarts s_bs;
-  __shared__ int s_first, s_last, s_qlo[2], s_qhi[2], s_bad;
+  __shared__ int s_first, s_last, s_qlo[2], s_qhi[2], s_qdead[2], s_bad;
   __shared__ int2 s_kdoc[kOwnDocTiles];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBOD + q), 1);
       s_qlo[q] = INT32_MAX;
       s_qhi[q] = -1;
+      s_qdead[q] = 0;
     }
     mbar_init(bar(kBDrain), 1);
     mbar_init(bar(kBDrain + 1), 1);
@@ -145,9 +146,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = threadIdx.x; i < 2 * p.tok; i += kThreads) {
       const int q = i / p.tok, t = tok0(q) + i % p.tok;
       if (q < nstream && t < a.Sq) {
-        const int id = max(doc_at(a, b, off + t, len), -1);
-        atomicMin(&s_qlo[q], id);
-        atomicMax(&s_qhi[q], id);
+        const int id = doc_at(a, b, off + t, len);
+        if (id < 0) {
+          s_qdead[q] = 1;
+        } else {
+          atomicMin(&s_qlo[q], id);
+          atomicMax(&s_qhi[q], id);
+        }
       }
     }
     if (own_docs)
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j0 > last_key(a, xb, len, prefix)) continue;
       bool whole = j0 + kTile - 1 <= last_key(a, xa, len, prefix);
       if (a.docs) {
-        const int2 kd = own_docs ? s_kdoc[t] : __ldg(p.kdoc + (int64_t)b * nkt + t), qd = make_int2(s_qlo[q], s_qhi[q]);
+        const int2 kd = own_docs ? s_kdoc[t] : __ldg(p.kdoc + (int64_t)b * nkt + t), qd = id_range(s_qlo[q], s_qhi[q], s_qdead[q]);
         if (!docs_meet(kd, qd)) continue;
         whole = whole && docs_one(kd, qd);
       }
