@@ -9,9 +9,9 @@
 //   warp 0      TMA producer: K, V once; Q, dO and the rows' statistics into a three-stage ring;
 //   warp 1      MMA issuer: S^T = K Q^T and dP^T = V dO^T, then for the sub-tile before dV += P^T dO, dK += dS^T Q and
 //               dQ^T = K^T dS^T;
-//   warps 2-9   one key row per thread, 32 of the sub-tile's 64 rows per warp: P^T and dS^T (16-bit) to tensor memory
+//   warps 4-11  one key row per thread, 32 of the sub-tile's 64 rows per warp: P^T and dS^T (16-bit) to tensor memory
 //               over S^T and dP^T, dS^T to shared memory too (the B operand of dQ^T);
-//   warps 10-13 dQ^T out of tensor memory, through a shared tile, to the fp32 accumulator with TMA reduce-add.
+//   warps 12-15 dQ^T out of tensor memory, through a shared tile, to the fp32 accumulator with TMA reduce-add.
 //
 // The bias's gradient: nearly every 32 x 32 block of pairs lies inside one bucket (distances beyond a few hundred share
 // few buckets): its sum goes to one number per warp.  A block across buckets is summed along its diagonals by rotating
@@ -33,7 +33,9 @@
 namespace lh {
 namespace bwd {
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 512;
+// Registers a thread of the issuing, computing and draining warps: 128 (48 + 2 * 184 + 96) = 512 * 128.
+constexpr int kRegsIssue = 48, kRegsCompute = 184, kRegsDrain = 96;
 constexpr int kQTile = 64;
 constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -152,7 +154,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const float q_out = F16 ? a.scale / (fs * kShift16) : a.scale;  // brings dQ and dK to scale
 
-  if (warp == 0) {
+  if (warp < 4) {
+   set_regs_dec<kRegsIssue>();
+   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0 && nit > 0) {
       bool ok = true;
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_teardown(bar(Lay::B_QF + it % kStages), (it / kStages) & 1);
       }
     }
-  } else if (warp == 1) {
+   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (the whole warp, one lane issuing)
     if (nit > 0) {
       constexpr int fmt = F16 ? kFmtF16 : kFmtBF16;
@@ -243,17 +247,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit_by(leader, bar(Lay::B_DRAIN));
       mbar_wait_teardown(bar(Lay::B_DRAIN), 0);
     }
-  } else if (warp < 10) {
+   }
+  } else if (warp < 12) {
     // ---------------------------------------------------------------- compute: P^T and dS^T
-    const int quarter = warp & 3, hc = (warp - 2) >> 2;
+    set_regs_inc<kRegsCompute>();
+    const int quarter = warp & 3, hc = (warp - 4) >> 2;
     const int r = quarter * 32 + lane;  // key row inside the tile = TMEM lane
-    const int tid = threadIdx.x - 64;
+    const int tid = threadIdx.x - 128;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const int key = k0 + r, kw = k0 + quarter * 32;  // this thread's key, the warp's first
     const int kid = doc_at(a, b, key, len);
     const bool kdead = kid < 0;
     const float mul = CAP ? a.cap * kLog2e : a.scale * kLog2e;
-    const float cap_in = 2.f * kLog2e * a.scale / (CAP ? a.cap : 1.f);
+    const float cap_in = a.scale / (CAP ? a.cap : 1.f);
     const uint64_t mul2 = f2pack(mul, mul);
     const int E = a.near, wide = 2 * E + 1;
     float bacc[4] = {0.f, 0.f, 0.f, 0.f};  // lane l: dtable sums of buckets l, l + 32, ...
@@ -302,8 +308,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tmem + 128 * i + 64 + lane_base + 32 * hc, dp);
         tmem_ld_wait();
         if (CAP) {
+          const float big = absmax32(sv, 0.f);
+          if (__all_sync(0xffffffffu, !(big * cap_in > 1.f))) {
+            const TanhPoly poly(1.f);
+            const uint64_t in2 = f2pack(cap_in, cap_in);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) sv[c] = fmaf(-2.f, rcp_approx(1.f + ex2(sv[c] * cap_in)), 1.f);
+            for (int c = 0; c < 32; c += 2) {
+              const uint64_t v = poly(mul_f32x2(f2pack(sv[c], sv[c + 1]), in2));
+              sv[c] = f2lo(v);
+              sv[c + 1] = f2hi(v);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sv[c] = tanh_any(sv[c] * cap_in);
+          }
         }
         uint32_t vis = 0xffffffffu;  // bit c: the pair (row0 + c, key) is visible
         if (!whole) {
@@ -430,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (BIAS == 2) {
         flush();
         float* out = p.w.dtpart +
-                     ((((int64_t)bh * p.nkt + kt) * a.G + (h0 - kvh * a.G + g)) * 8 + (warp - 2)) * a.buckets;
+                     ((((int64_t)bh * p.nkt + kt) * a.G + (h0 - kvh * a.G + g)) * 8 + (warp - 4)) * a.buckets;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           if (lane + 32 * m < a.buckets) out[lane + 32 * m] = F16 ? bacc[m] / kShift16 : bacc[m];
@@ -475,9 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- drain: dQ^T -> shared tile -> TMA reduce-add
+    set_regs_dec<kRegsDrain>();
     const int quarter = warp & 3;
     const int f = quarter * 32 + lane;  // feature = TMEM lane of dQ^T
-    const int dt = threadIdx.x - 320;
+    const int dt = threadIdx.x - 384;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     float* stage = reinterpret_cast<float*>(smem + Lay::DQ);
     bool ok = true;
