@@ -244,7 +244,8 @@ int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTens
 
 // Backward: workspace buffers.
 struct DenseBwdBuf {
-  float* stats;         // [2][B Hq][Sq rounded up to 4]: -LSE log2(e) (fp16: + 12; -inf for a dead row), -D
+  float* stats;         // [2][B Hq][Sq rounded up to 4]: -LSE log2(e) (fp16: + 12; slopes: - slope (i mod 64) log2(e);
+                        // -inf for a dead row), -D
   unsigned int* amax;   // [B Hkv][2] bits of the largest |dO_i| and |V_j| (fp16 only; zeroed by the caller)
   float* dqacc;         // fp32 [B Hq][Sq][d]
   float* dkv;           // fp32 [shares][dV, dK][B Hkv][Skv][d], where the query heads of a key head are shared out

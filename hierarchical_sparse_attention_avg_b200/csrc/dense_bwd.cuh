@@ -27,6 +27,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "dense.cuh"
 
@@ -333,49 +334,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * Lay::ST) + 8 * hc;
         const ulonglong2* nd4 = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * Lay::ST + kQTile * 4) + 8 * hc;
         const int d0 = x0 - key;  // distance of column 0
-        const float fd0 = (float)d0;
-        if (BIAS == 1 && !near) badd = slope2 * fd0;
-        const uint64_t badd2 = f2pack(badd, badd), ns2 = f2pack(slope2, slope2);
+        // a tile on one side of the slopes: the statistics hold the columns' share, this is the key's and the tile's
+        if (BIAS == 1 && !near) badd = slope2 * (float)(d0 - 32 * hc);
+        const uint64_t badd2 = f2pack(badd, badd);
         uint64_t sum2 = 0ull;
+        // P and dS of the 32 columns; Near: the bias differs from pair to pair
+        auto columns = [&](auto tag) {
+          constexpr bool Near = decltype(tag)::value;
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const ulonglong2 nl = nl4[c >> 2], nd = nd4[c >> 2];
+          for (int c = 0; c < 32; c += 4) {
+            const ulonglong2 nl = nl4[c >> 2], nd = nd4[c >> 2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int cc = c + 2 * h;
-            uint64_t arg = fma_f32x2(f2pack(sv[cc], sv[cc + 1]), mul2, h ? nl.y : nl.x);
-            if (BIAS == 1) {
-              uint64_t bb;
-              if (near) bb = f2pack(slope2 * fabsf(fd0 + cc), slope2 * fabsf(fd0 + (cc + 1)));
-              else bb = fma_f32x2(f2pack((float)cc, (float)(cc + 1)), ns2, badd2);
-              arg = add_f32x2(arg, bb);
+            for (int h = 0; h < 2; ++h) {
+              const int cc = c + 2 * h;
+              uint64_t arg = fma_f32x2(f2pack(sv[cc], sv[cc + 1]), mul2, h ? nl.y : nl.x);
+              if (BIAS != 0 && !Near) arg = add_f32x2(arg, badd2);
+              if (BIAS == 1 && Near) {
+                auto bb = [&](int e) { return slope2 * (fabsf((float)(d0 + e)) - (float)(32 * hc + e)); };
+                arg = add_f32x2(arg, f2pack(bb(cc), bb(cc + 1)));
+              }
+              if (BIAS == 2 && Near)
+                arg = add_f32x2(arg, f2pack(__ldg(bias + min(max(d0 + cc, -E), E)), __ldg(bias + min(max(d0 + cc + 1, -E), E))));
+              const float p0 = ex2(f2lo(arg)), p1 = ex2(f2hi(arg));
+              uint64_t z2 = mul_f32x2(f2pack(p0, p1), add_f32x2(f2pack(dp[cc], dp[cc + 1]), h ? nd.y : nd.x));
+              pk[cc / 2] = pack2_rn<F16>(p0, p1);
+              if (BIAS == 2) {
+                sum2 = add_f32x2(sum2, z2);
+                dp[cc] = f2lo(z2);
+                dp[cc + 1] = f2hi(z2);
+              }
+              if (CAP) {
+                const uint64_t t2 = f2pack(sv[cc], sv[cc + 1]), nt2 = f2pack(-sv[cc], -sv[cc + 1]);
+                z2 = mul_f32x2(z2, fma_f32x2(t2, nt2, f2pack(1.f, 1.f)));
+              }
+              if (F16) z2 = mul_f32x2(z2, f2pack(fs, fs));
+              dk[cc / 2] = pack2_rn<F16>(f2lo(z2), f2hi(z2));
             }
+          }
+        };
+        if (BIAS != 0 && near) columns(std::true_type{});
+        else columns(std::false_type{});
+        if (!whole) {  // masked pairs are nothing, whatever came out
+          sum2 = 0ull;
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const uint32_t m = (vis >> c & 1 ? 0xffffu : 0u) | (vis >> (c + 1) & 1 ? 0xffff0000u : 0u);
+            pk[c / 2] &= m;
+            dk[c / 2] &= m;
             if (BIAS == 2) {
-              uint64_t bb = badd2;
-              if (near)
-                bb = f2pack(__ldg(bias + min(max(d0 + cc, -E), E)), __ldg(bias + min(max(d0 + cc + 1, -E), E)));
-              arg = add_f32x2(arg, bb);
+              dp[c] = vis >> c & 1 ? dp[c] : 0.f;
+              dp[c + 1] = vis >> (c + 1) & 1 ? dp[c + 1] : 0.f;
+              sum2 = add_f32x2(sum2, f2pack(dp[c], dp[c + 1]));
             }
-            float p0 = ex2(f2lo(arg)), p1 = ex2(f2hi(arg));
-            uint64_t z2 = mul_f32x2(f2pack(p0, p1), add_f32x2(f2pack(dp[cc], dp[cc + 1]), h ? nd.y : nd.x));
-            if (!whole) {
-              const bool v0 = vis >> cc & 1, v1 = vis >> (cc + 1) & 1;
-              p0 = v0 ? p0 : 0.f;
-              p1 = v1 ? p1 : 0.f;
-              z2 = f2pack(v0 ? f2lo(z2) : 0.f, v1 ? f2hi(z2) : 0.f);
-            }
-            pk[cc / 2] = pack2_rn<F16>(p0, p1);
-            if (BIAS == 2) {
-              sum2 = add_f32x2(sum2, z2);
-              dp[cc] = f2lo(z2);
-              dp[cc + 1] = f2hi(z2);
-            }
-            if (CAP) {
-              const uint64_t t2 = f2pack(sv[cc], sv[cc + 1]), nt2 = f2pack(-sv[cc], -sv[cc + 1]);
-              z2 = mul_f32x2(z2, fma_f32x2(t2, nt2, f2pack(1.f, 1.f)));
-            }
-            if (F16) z2 = mul_f32x2(z2, f2pack(fs, fs));
-            dk[cc / 2] = pack2_rn<F16>(f2lo(z2), f2hi(z2));
           }
         }
         if (it >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::B_MM + i), ((it >> 1) - 1) & 1, &s_wait, status));

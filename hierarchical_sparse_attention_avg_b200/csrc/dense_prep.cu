@@ -62,7 +62,10 @@ __device__ __forceinline__ void bwd_row(const DenseDims& a, const DenseTensor& o
     dead = l == -INFINITY || doc_at(a, b, len - a.Sq + i, len) < 0;
     if (f == 0) {
       const int64_t pitch = (a.Sq + 3) & ~3, at = bh * pitch + i;
-      w.stats[at] = dead ? -INFINITY : fmaf(l, -1.4426950408889634f, F16 ? 12.f : 0.f);
+      // -LSE log2(e); with slopes also the share of the row's place in its 64-row sub-tile, - slope (i mod 64) log2(e)
+      const float nl = fmaf(l, -1.4426950408889634f, F16 ? 12.f : 0.f);
+      const float sl = a.slopes ? -1.4426950408889634f * __ldg(a.slopes + h) * (float)(i & 63) : 0.f;
+      w.stats[at] = dead ? -INFINITY : nl + sl;
       w.stats[(int64_t)a.B * a.Hq * pitch + at] = dead ? 0.f : -dot;
     }
   }
