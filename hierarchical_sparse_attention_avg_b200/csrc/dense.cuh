@@ -104,11 +104,11 @@ __device__ __forceinline__ uint32_t same_doc(int other, int mine) {
   return same;
 }
 
-// tanh, |error| <= about 2e-7 both ways (the hardware's tanh has 5e-4: times a cap of 50 a score off by 0.02, more than
-// the operands' own rounding gives).  Where a thread's arguments are all within [-1, 1] (scores below the cap, nearly
-// always), an odd polynomial on pairs, x p(x^2) with p fitted to tanh(x) / x for the least |error| of tanh on [0, 1]
-// (weighted least squares, weights raised where the error was large): 9 packed FMAs a pair, against two exponentials and
-// two reciprocals, whose pipe the softmax itself fills.
+// tanh, |error| <= about 2e-7 every way (the hardware's tanh has 5e-4: times a cap of 50 a score off by 0.02, more than
+// the operands' own rounding gives).  Where a warp's arguments are all small (scores below the cap, nearly always), an odd
+// polynomial on pairs, x p(x^2) with p fitted to tanh(x) / x for the least |error| of tanh (weighted least squares, the
+// weights raised where the error was large): on [0, 1/2] with 4 coefficients 1.6e-7, on [0, 1] with 7 coefficients 0.9e-7;
+// 6 or 9 packed FMAs a pair, against two exponentials and two reciprocals, whose pipe the softmax itself fills.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -117,22 +117,44 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ float tanh_any(float x) {
   return fmaf(-2.f, rcp_approx(1.f + ex2(x * (2.f * 1.4426950408889634f))), 1.f);
 }
+template <bool Half>
 struct TanhPoly {  // f * tanh
-  uint64_t c[7];
+  static constexpr int N = Half ? 4 : 7;
+  uint64_t c[N];
   __device__ __forceinline__ explicit TanhPoly(float f) {
-    const float k[7] = {0.999999693f, -0.333321293f, 0.133195837f, -0.053265835f, 0.0199732811f, -0.00595127819f,
-                        0.000963771153f};
+    const float k4[4] = {0.999997677f, -0.33320657f, 0.131451624f, -0.0433729225f};
+    const float k7[7] = {0.999999693f, -0.333321293f, 0.133195837f, -0.053265835f, 0.0199732811f, -0.00595127819f,
+                         0.000963771153f};
 #pragma unroll
-    for (int i = 0; i < 7; ++i) c[i] = f2pack(k[i] * f, k[i] * f);
-  }
-  __device__ __forceinline__ uint64_t operator()(uint64_t x) const {
-    const uint64_t u = mul_f32x2(x, x);
-    uint64_t y = c[6];
-#pragma unroll
-    for (int i = 5; i >= 0; --i) y = fma_f32x2(y, u, c[i]);
-    return mul_f32x2(y, x);
+    for (int i = 0; i < N; ++i) c[i] = f2pack((Half ? k4[i % 4] : k7[i]) * f, (Half ? k4[i % 4] : k7[i]) * f);
   }
 };
+// f tanh(in v) of 32 values, all of magnitude <= 1/2 (Half) or 1 after the scaling.
+template <bool Half>
+__device__ __forceinline__ void tanh32(float (&v)[32], float in, float f) {
+  const TanhPoly<Half> poly(f);
+  const uint64_t in2 = f2pack(in, in);
+#pragma unroll
+  for (int i = 0; i < 32; i += 16) {  // eight pairs side by side: a chain alone would wait for each of its steps
+    uint64_t x[8], u[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = mul_f32x2(f2pack(v[i + 2 * e], v[i + 2 * e + 1]), in2);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = mul_f32x2(x[e], x[e]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fma_f32x2(poly.c[TanhPoly<Half>::N - 1], u[e], poly.c[TanhPoly<Half>::N - 2]);
+#pragma unroll
+    for (int k = TanhPoly<Half>::N - 3; k >= 0; --k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = fma_f32x2(y[e], u[e], poly.c[k]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t t = mul_f32x2(y[e], x[e]);
+      v[i + 2 * e] = f2lo(t);
+      v[i + 2 * e + 1] = f2hi(t);
+    }
+  }
+}
 // Largest magnitude of 32 values against m.
 __device__ __forceinline__ float absmax32(const float (&v)[32], float m) {
   float a = m, b = 0.f, c = 0.f, d = 0.f;
@@ -166,9 +188,9 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return F16 ? (((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u) : (((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u);
 }
 
-// o's 16-bit row chunk of 8 features, and what its rounding dropped (low may be null).
+// 8 features as 16-bit values, and what the rounding dropped.
 template <bool F16>
-__device__ __forceinline__ void store8(uint16_t* o, uint16_t* low, const float* v) {
+__device__ __forceinline__ uint4 round8(const float* v, uint4* low) {
   uint32_t w[4], r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -176,9 +198,30 @@ __device__ __forceinline__ void store8(uint16_t* o, uint16_t* low, const float* 
     const float2 u = unpack2<F16>(w[i]);
     r[i] = pack2_rn<F16>(v[2 * i] - u.x, v[2 * i + 1] - u.y);
   }
-  st16(o, make_uint4(w[0], w[1], w[2], w[3]));
-  if (low) st16(low, make_uint4(r[0], r[1], r[2], r[3]));
+  *low = make_uint4(r[0], r[1], r[2], r[3]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// A warp's 32 result rows on their way out, 128 bytes of each at a time, through 4 KB of shared memory: a thread has a row,
+// and storing it from there writes 32 rows at 16 bytes apiece (15,000 cycles for a 128 x 128 tile and its low half); out of
+// shared memory eight lanes write 128 bytes of one row.
+struct RowStage {
+  uint8_t* buf;
+  __device__ __forceinline__ uint4* at(int row, int chunk) const {
+    return reinterpret_cast<uint4*>(buf + row * 128 + ((chunk ^ (row & 7)) << 4));
+  }
+  // The rows in `valid` go to dst, each lane's own row's place.
+  __device__ __forceinline__ void flush(uint32_t valid, void* dst, int lane) const {
+    __syncwarp();
+#pragma unroll 4
+    for (int r = 0; r < 32; r += 4) {
+      const int row = r + (lane >> 3), c = lane & 7;
+      uint8_t* p = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+      if (valid >> row & 1) st16(p + 16 * c, *at(row, c));
+    }
+    __syncwarp();
+  }
+};
 
 // Tensor-core instructions of a converged issuer warp: every lane runs the issuing code with the same values, so that
 // descriptors stay in uniform registers, and the one lane with `leader` set issues.

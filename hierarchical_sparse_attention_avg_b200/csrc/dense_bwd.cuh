@@ -309,16 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tmem + 128 * i + 64 + lane_base + 32 * hc, dp);
         tmem_ld_wait();
         if (CAP) {
-          const float big = absmax32(sv, 0.f);
-          if (__all_sync(0xffffffffu, !(big * cap_in > 1.f))) {
-            const TanhPoly poly(1.f);
-            const uint64_t in2 = f2pack(cap_in, cap_in);
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const uint64_t v = poly(mul_f32x2(f2pack(sv[c], sv[c + 1]), in2));
-              sv[c] = f2lo(v);
-              sv[c + 1] = f2hi(v);
-            }
+          const float big = absmax32(sv, 0.f) * cap_in;
+          if (__all_sync(0xffffffffu, big <= 0.5f)) {
+            tanh32<true>(sv, cap_in, 1.f);
+          } else if (__all_sync(0xffffffffu, big <= 1.f)) {
+            tanh32<false>(sv, cap_in, 1.f);
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) sv[c] = tanh_any(sv[c] * cap_in);
@@ -477,6 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint16_t* dst = static_cast<uint16_t*>(hc == 0 ? p.dv : p.dk) + b * st.b + kvh * st.h + key * st.s;
       // with the query heads shared out, fp32 sums [share][dV, dK][B Hkv][Skv][d], added by another kernel
       float* part = p.w.dkv ? p.w.dkv + ((((int64_t)blockIdx.z * 2 + hc) * a.B * a.Hkv + bh) * a.Skv + key) * D : nullptr;
+      const RowStage stage{smem + (hc == 0 ? Lay::K : Lay::V) + quarter * (Lay::KT / 4)};  // (K and V are consumed)
+      const uint32_t rows = __ballot_sync(0xffffffffu, key < a.Skv);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
@@ -486,18 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = nit > 0 ? v[e] * f : 0.f;
-        if (key < a.Skv) {
-          if (part) {
+        if (part) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(part + c * 32 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-          } else {
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(stage.at(lane, e)) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          stage.flush(rows, part + 32 * c, lane);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + c * 32 + e) =
-                  make_uint4(pack2_rn<F16>(v[e], v[e + 1]), pack2_rn<F16>(v[e + 2], v[e + 3]),
-                             pack2_rn<F16>(v[e + 4], v[e + 5]), pack2_rn<F16>(v[e + 6], v[e + 7]));
+          for (int e = 0; e < 4; ++e) {
+            uint4 lo;
+            *stage.at(lane, 4 * (c & 1) + e) = round8<F16>(v + 8 * e, &lo);
           }
+          if (c & 1) stage.flush(rows, dst + 32 * (c - 1), lane);
         }
       }
     }

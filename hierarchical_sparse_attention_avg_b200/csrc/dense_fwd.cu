@@ -58,7 +58,9 @@ __global__ void __launch_bounds__(128) join_kernel(const float* __restrict__ par
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       v[e] = ((s_acc[0][i + e] + s_acc[1][i + e]) + (s_acc[2][i + e] + s_acc[3][i + e])) * inv;
-    store8<F16>(at(o) + i, low.p ? at(low) + i : nullptr, v);
+    uint4 lo;
+    st16(at(o) + i, round8<F16>(v, &lo));
+    if (low.p) st16(at(low) + i, lo);
   }
   if (threadIdx.x == 0) lse[row] = lt == 0.f ? -INFINITY : (m + __log2f(lt)) * kLn2;
 }

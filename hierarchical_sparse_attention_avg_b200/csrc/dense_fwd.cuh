@@ -57,7 +57,7 @@ constexpr int kSees = 1, kMasked = 4, kNear = 16, kBad = 64;
 // Registers a thread: 128 * 56 + 256 * 224 = 384 * 168, what the block is launched with.
 constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
 
-enum { kBQ = 0, kBFull = 1, kBFree = kBFull + kMaxSlots, kBSF = kBFree + kMaxSlots, kBPF = kBSF + 2, kBOD = kBPF + 2,
+enum { kBQ = 0, kBFull = 1, kBFree = kBFull + kMaxSlots, kBSF = kBFree + kMaxSlots, kBPF = kBSF + 2, kBOD = kBPF + 4,
        kBDrain = kBOD + 2, kNBar = kBDrain + 2 };
 
 struct FwdArgs {
@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = 0; q < 2; ++q) {
       mbar_init(bar(kBSF + q), 1);
       mbar_init(bar(kBPF + q), kTile);
+      mbar_init(bar(kBPF + 2 + q), kTile);
       mbar_init(bar(kBOD + q), 1);
       s_qlo[q] = INT32_MAX;
       s_qhi[q] = -1;
@@ -262,12 +263,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit_by(leader, bar(kBSF + q));
       };
-      auto values = [&](int q, int slot, bool add) {  // O_q (+)= P_q V
+      // O_q (+)= P_q V, the keys of each half of the tile as soon as their probabilities are there
+      auto values = [&](int q, int slot, bool add, uint32_t ph) {
         const uint64_t v0 = dV + slot * (TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_ts_by(leader, tm + 256 + 128 * q, tm + 128 * q + kk * 8, v0 + kk * (2048 >> 4), idesc_pv,
-                     (add || kk > 0) ? 1u : 0u);
+        for (int hh = 0; hh < 2; ++hh) {
+          if (!wait(kBPF + 2 * hh + q, ph)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4 * hh; kk < 4 * hh + 4; ++kk)
+            umma_ts_by(leader, tm + 256 + 128 * q, tm + 128 * q + kk * 8, v0 + kk * (2048 >> 4), idesc_pv,
+                       (add || kk > 0) ? 1u : 0u);
+        }
+        return true;
       };
       // A stream's next scores are issued right behind its product: they overwrite P once the product has read it, and
       // their commit tells the softmax that the product is done.
@@ -285,10 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit_by(leader, bar(kBFree + s0 + r.s));
             r.step(p.slots);
           }
-          ok = wait(kBFull + s0 + r.s, r.ph) && wait(kBPF + me, n & 1);
+          ok = wait(kBFull + s0 + r.s, r.ph) && values(me, s0 + r.s, n > 0, n & 1);
           if (!ok) break;
-          tc_fence_after();
-          values(me, s0 + r.s, n > 0);
           umma_commit_by(leader, bar(kBFree + s0 + r.s));
           r.step(p.slots);
           t = next(t, mask);
@@ -324,12 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             if (ok && (f >> q & 1)) {
-              ok = wait(kBPF + q, cnt[q] & 1);
-              if (ok) {
-                tc_fence_after();
-                values(q, sv, cnt[q] > 0);
-                ++cnt[q];
-              }
+              ok = values(q, sv, cnt[q] > 0, cnt[q] & 1);
+              ++cnt[q];
             }
             if (ok && (fa >> q & 1)) {
               if (!k_here) ok = wait(kBFull + r.s, r.ph);
@@ -412,6 +414,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBSF + q), cnt & 1, &s_wait, status));
         if (!ok) continue;  // (the group's later barriers still count this warp)
         tc_fence_after();
+        if (masked) {  // value rows that may meet a probability of zero: clear what is not finite (thread = row)
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(kBFull + ring + r.s), r.ph, &s_wait, status));
+          if (!ok) continue;  // (the group's later barriers still count this warp)
+          uint8_t* vr = smem + p.off_kv + (ring + r.s) * TILE + row * 128;
+          uint32_t bad = 0;
+          if (!dead) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 w = *reinterpret_cast<const uint4*>(vr + (i >> 3) * 16384 + (((i + lane) & 7) << 4));
+              bad |= nonfinite2<F16>(w.x) | nonfinite2<F16>(w.y) | nonfinite2<F16>(w.z) | nonfinite2<F16>(w.w);
+            }
+          }
+          if (dead) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              *reinterpret_cast<uint4*>(vr + (i >> 3) * 16384 + (((i + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          } else if (bad) {
+#pragma unroll 1
+            for (int i = 0; i < D; ++i) {
+              unsigned short* e = reinterpret_cast<unsigned short*>(vr + (i >> 6) * 16384) + (i & 63);
+              if (nonfinite2<F16>(*e)) *e = 0;
+            }
+            atomicOr(reinterpret_cast<unsigned int*>(flags) + ((t - ks) >> 2), (unsigned)(kBad << q) << (8 * ((t - ks) & 3)));
+            s_bad = 1;
+          }
+          fence_proxy_async_smem();
+        }
         if (active) {
           float s[CH][32];
 #pragma unroll
@@ -424,17 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < CH; ++c) big = absmax32(s[c], big);
             }
-            if (REP == 1 && __all_sync(0xffffffffu, !valid || big * cap_in <= 1.f)) {
-              const TanhPoly poly(mul0);
-              const uint64_t in2 = f2pack(cap_in, cap_in);
+            big *= cap_in;
+            if (REP == 1 && __all_sync(0xffffffffu, !valid || big <= 1.f)) {
 #pragma unroll
-              for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  const uint64_t v = poly(mul_f32x2(f2pack(s[c][i], s[c][i + 1]), in2));
-                  s[c][i] = f2lo(v);
-                  s[c][i + 1] = f2hi(v);
-                }
+              for (int c = 0; c < CH; ++c) tanh32<false>(s[c], cap_in, mul0);
               mul = 1.f;
             } else {
 #pragma unroll
@@ -518,6 +540,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             l_run *= alpha;
             m_run = m_new;
           }
+          // O_q's last product has completed (it was issued before these scores): bring O_q to the new maximum
+          if (cnt > 0 && move) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(tO + c * 32, o);
+            }
+          }
           // P over the first 64 columns of S, and its row sum; a row that has seen no key yet keeps P = 0
           const float sub = cadd - (m_run == -INFINITY ? 0.f : m_run);
           uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
@@ -535,6 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 64; i += 2) pk[i / 2] = __uint_as_float(pair(2 * hh + i / 32, i % 32));
               tmem_st32(tS + 32 * hh, pk);
+              if (hh == 0) {  // the product may start on the first 64 keys
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(bar(kBPF + q));
+              }
             }
           } else {  // the other copies' columns are theirs: zeros here
             uint32_t pk[16];
@@ -546,52 +585,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (e != quarter) tmem_st16(tS + 16 * e, zero);
             tmem_st16(tS + 16 * quarter, pk);
           }
-          // O_q's last product has completed (it was issued before these scores): bring O_q to the new maximum
-          if (cnt > 0 && move) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld32(tO + c * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tmem_st32(tO + c * 32, o);
-            }
-          }
           tmem_st_wait();
+          tc_fence_before();
+          if (REP != 1) mbar_arrive(bar(kBPF + q));
+          mbar_arrive(bar(kBPF + 2 + q));
           float rs[8] = {f2lo(rs2[0]), f2hi(rs2[0]), f2lo(rs2[1]), f2hi(rs2[1]),
                          f2lo(rs2[2]), f2hi(rs2[2]), f2lo(rs2[3]), f2hi(rs2[3])};
           l_run += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
         }
-        if (masked) {  // value rows that may meet a probability of zero: clear what is not finite (thread = row)
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(kBFull + ring + r.s), r.ph, &s_wait, status));
-          if (!ok) continue;
-          uint8_t* vr = smem + p.off_kv + (ring + r.s) * TILE + row * 128;
-          uint32_t bad = 0;
-          if (!dead) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              const uint4 w = *reinterpret_cast<const uint4*>(vr + (i >> 3) * 16384 + (((i + lane) & 7) << 4));
-              bad |= nonfinite2<F16>(w.x) | nonfinite2<F16>(w.y) | nonfinite2<F16>(w.z) | nonfinite2<F16>(w.w);
-            }
-          }
-          if (dead) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<uint4*>(vr + (i >> 3) * 16384 + (((i + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          } else if (bad) {
-#pragma unroll 1
-            for (int i = 0; i < D; ++i) {
-              unsigned short* e = reinterpret_cast<unsigned short*>(vr + (i >> 6) * 16384) + (i & 63);
-              if (nonfinite2<F16>(*e)) *e = 0;
-            }
-            atomicOr(reinterpret_cast<unsigned int*>(flags) + ((t - ks) >> 2), (unsigned)(kBad << q) << (8 * ((t - ks) & 3)));
-            s_bad = 1;
-          }
-          fence_proxy_async_smem();
+        if (!active) {
+          tc_fence_before();
+          mbar_arrive(bar(kBPF + q));
+          mbar_arrive(bar(kBPF + 2 + q));
         }
-        tc_fence_before();
-        mbar_arrive(bar(kBPF + q));
         ++cnt;
       }
 
@@ -602,21 +608,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const bool part = p.nsplit > 1;
-      // features [f0, f0 + n) of a row: n = 32 or 16 fp32 values
-      auto store = [&](int64_t ri, int hh, int tt, int f0, int n, const float* v) {
-        if (part) {
-          float* dst = p.part_o + ((int64_t)split * a.B * a.Hq * a.Sq + ri) * D + f0;
-#pragma unroll
-          for (int i = 0; i < n; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        } else {
-          auto at = [&](const DenseTensor& t) {
-            return static_cast<uint16_t*>(const_cast<void*>(t.p)) + b * t.st.b + hh * t.st.h + (int64_t)tt * t.st.s + f0;
-          };
-          uint16_t *od = at(p.o), *ld = p.low.p ? at(p.low) : nullptr;
-#pragma unroll
-          for (int i = 0; i < n; i += 8) store8<F16>(od + i, ld ? ld + i : nullptr, v + i);
-        }
+      auto out = [&](const DenseTensor& t, int hh, int tt) {  // a row's place in o or low
+        return t.p ? static_cast<uint16_t*>(const_cast<void*>(t.p)) + b * t.st.b + hh * t.st.h + (int64_t)tt * t.st.s
+                   : nullptr;
       };
+      const int64_t pbase = (int64_t)split * a.B * a.Hq * a.Sq;  // rows of the splits before this one
       // values that are not finite, of the keys that the row sees (rare): v's features [f0, f0 + n) with them added
       auto add_bad = [&](int jl, int doc, int f0, int n, float* v) {
         if (!*static_cast<volatile int*>(&s_bad)) return;
@@ -634,13 +630,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto stats = [&](int64_t ri, float m, float l) {
         const float l2 = l == 0.f ? -INFINITY : m + __log2f(l);
-        if (part) p.part_lse[(int64_t)split * a.B * a.Hq * a.Sq + ri] = l2;
+        if (part) p.part_lse[pbase + ri] = l2;
         else p.lse[ri] = l2 * kLn2;
       };
       if constexpr (REP == 1) {
         float a0 = 1.f, a1 = 0.f;
         float* so = reinterpret_cast<float*>(smem + p.off_kv);  // [D][128] of stream 1 (keys and values are consumed)
-        float* sm = reinterpret_cast<float*>(smem);             // [2][128] its maxima and sums (the queries too)
+        float* sm = so + D * kTile;                             // [2][128] its maxima and sums
         if (p.dual) {
           if (q == 1 && ok && active) {
             sm[row] = m_run;
@@ -673,6 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
           const int64_t ri = ((int64_t)b * a.Hq + h) * a.Sq + tk;
           const bool use0 = cnt > 0 && inv != 0.f, use1 = p.dual && a1 != 0.f && inv != 0.f;
+          const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+          const RowStage stage{smem + (p.dual ? 0 : q) * TILE + quarter * 4096};  // (the queries are consumed)
+          uint16_t *orow = out(p.o, h, tk), *lrow = out(p.low, h, tk);
+          float* prow = part ? p.part_o + (pbase + ri) * D : nullptr;
+          uint4 lo[8];
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
@@ -686,9 +687,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = fmaf(so[(c * 32 + i) * kTile + row], a1 * inv, o[i]);
             }
-            if (valid) {
-              add_bad(jlast, mydoc, c * 32, 32, o);
-              store(ri, h, tk, c * 32, 32, o);
+            if (valid) add_bad(jlast, mydoc, c * 32, 32, o);
+            if (part) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(stage.at(lane, i)) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              stage.flush(rows, prow + 32 * c, lane);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) *stage.at(lane, 4 * (c & 1) + i) = round8<F16>(o + 8 * i, lo + 4 * (c & 1) + i);
+              if (c & 1) {
+                stage.flush(rows, orow + 32 * (c - 1), lane);
+                if (p.low.p) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) *stage.at(lane, i) = lo[i];
+                  stage.flush(rows, lrow + 32 * (c - 1), lane);
+                }
+              }
             }
           }
           if (valid) stats(ri, m_run, l_run);
@@ -735,7 +750,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           const int64_t ri = ((int64_t)b * a.Hq + h) * a.Sq + tk;
           add_bad(jlast, mydoc, me * N, N, o);
-          store(ri, h, tk, me * N, N, o);
+          if (part) {
+            float* dst = p.part_o + (pbase + ri) * D + me * N;
+#pragma unroll
+            for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else {
+            uint16_t *od = out(p.o, h, tk) + me * N, *ld = out(p.low, h, tk);
+#pragma unroll
+            for (int i = 0; i < N; i += 8) {
+              uint4 lo;
+              st16(od + i, round8<F16>(o + i, &lo));
+              if (ld) st16(ld + me * N + i, lo);
+            }
+          }
           if (me == 0) stats(ri, m, l);
         }
       }

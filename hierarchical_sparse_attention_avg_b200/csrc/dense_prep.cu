@@ -188,13 +188,18 @@ __device__ __forceinline__ void dtable_rows(const DenseDims& a, const float* __r
   const int kvh = h / a.G, g = h % a.G, k = k0 + threadIdx.x % 32, w = threadIdx.x / 32;
   __shared__ double s_sum[8][32];
   double sum = 0.0;
-  if (k < a.buckets)
-    for (int b = 0; b < a.B; ++b) {
-      const float* src = part + ((((int64_t)b * a.Hkv + kvh) * nkt * a.G + g) * 8 + w) * a.buckets + k;
-      const int64_t step = (int64_t)a.G * 8 * a.buckets;
+  if (k < a.buckets) {
+    const int64_t step = (int64_t)a.G * 8 * a.buckets, jump = (int64_t)(a.Hkv - 1) * nkt * step;
+    const float* src = part + (((int64_t)kvh * nkt * a.G + g) * 8 + w) * a.buckets + k;
+    const int total = a.B * nkt;
+    int kt = 0;
 #pragma unroll 8
-      for (int kt = 0; kt < nkt; ++kt) sum += src[kt * step];
+    for (int t = 0; t < total; ++t) {
+      sum += *src;
+      src += step;
+      if (++kt == nkt) kt = 0, src += jump;  // the next batch entry
     }
+  }
   s_sum[w][threadIdx.x % 32] = sum;
   __syncthreads();
   if (w == 0 && k < a.buckets) {

@@ -558,8 +558,6 @@ def _rows(t, shape, dtype, device, name) -> bytes:
 
 
 def _vec(t, shape, dtype, device, name) -> int:
-    if t is None:
-        return 0
     if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -567,11 +565,11 @@ def _vec(t, shape, dtype, device, name) -> int:
 
 
 def _attn_mods(P: AttnParams, dev, slopes, table, docs, prefix, kv_len) -> bytes:
-    return _pack_mods(_vec(slopes, (P.Hq,), torch.float32, dev, "slopes"),
-                      _vec(table, (P.Hq, P.buckets), P.dtype, dev, "table"),
-                      _vec(docs, (P.B, P.Skv), torch.int32, dev, "docs"),
-                      _vec(prefix, (P.B,), torch.int32, dev, "prefix"),
-                      _vec(kv_len, (P.B,), torch.int32, dev, "kv_len"))
+    return _pack_mods(0 if slopes is None else _vec(slopes, (P.Hq,), torch.float32, dev, "slopes"),
+                      0 if table is None else _vec(table, (P.Hq, P.buckets), P.dtype, dev, "table"),
+                      0 if docs is None else _vec(docs, (P.B, P.Skv), torch.int32, dev, "docs"),
+                      0 if prefix is None else _vec(prefix, (P.B,), torch.int32, dev, "prefix"),
+                      0 if kv_len is None else _vec(kv_len, (P.B,), torch.int32, dev, "kv_len"))
 
 
 def _attn_ws(P: AttnParams, ws, dev, backward, where):
@@ -607,9 +605,9 @@ def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, 
     ws = _attn_ws(P, ws, dev, False, "lh_attn_forward")
     qs, ks = P._qs, P._ks
     if o is None:
-        o = torch.empty(qs, dtype=P.dtype, device=dev)
+        o = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty(qs[:3], dtype=torch.float32, device=dev)
+        lse = q.new_empty(qs[:3], dtype=torch.float32)
     dt = P.dtype
     rc = _on_device(dev, _lib.lh_attn_forward, P._ref, _attn_mods(P, dev, slopes, table, docs, prefix, kv_len),
                     _rows(q, qs, dt, dev, "q"), _rows(k, ks, dt, dev, "k"), _rows(v, ks, dt, dev, "v"),
@@ -627,17 +625,17 @@ def lh_attn_backward(P: AttnParams, q, k, v, o, lse, dout, slopes=None, table=No
     dev = q.device
     ws = _attn_ws(P, ws, dev, True, "lh_attn_backward")
     qs, ks = P._qs, P._ks
-    dq = torch.empty(qs, dtype=P.dtype, device=dev) if dq is None else dq
-    dk = torch.empty(ks, dtype=P.dtype, device=dev) if dk is None else dk
-    dv = torch.empty(ks, dtype=P.dtype, device=dev) if dv is None else dv
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
     if P.buckets and dtable is None:
-        dtable = torch.empty((P.Hq, P.buckets), dtype=P.dtype, device=dev)
+        dtable = torch.empty_like(table)
     dt = P.dtype
     rc = _on_device(dev, _lib.lh_attn_backward, P._ref, _attn_mods(P, dev, slopes, table, docs, prefix, kv_len),
                     _rows(q, qs, dt, dev, "q"), _rows(k, ks, dt, dev, "k"), _rows(v, ks, dt, dev, "v"),
                     _rows(o, qs, dt, dev, "o"), None if low is None else _rows(low, qs, dt, dev, "low"),
                     _vec(lse, qs[:3], torch.float32, dev, "lse"), _rows(dout, qs, dt, dev, "dout"),
                     _rows(dq, qs, dt, dev, "dq"), _rows(dk, ks, dt, dev, "dk"), _rows(dv, ks, dt, dev, "dv"),
-                    _vec(dtable, (P.Hq, P.buckets), dt, dev, "dtable"), ws.data_ptr(), ws.numel())
+                    _vec(dtable, (P.Hq, P.buckets), dt, dev, "dtable") if P.buckets else 0, ws.data_ptr(), ws.numel())
     _check(rc, "lh_attn_backward")
     return dq, dk, dv, dtable
