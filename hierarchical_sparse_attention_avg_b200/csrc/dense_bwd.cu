@@ -4,10 +4,10 @@
 namespace lh {
 namespace bwd {
 
-extern template int launch<64, false>(const CUtensorMap (&)[6], const BwdArgs&, cudaStream_t);
-extern template int launch<64, true>(const CUtensorMap (&)[6], const BwdArgs&, cudaStream_t);
-extern template int launch<128, false>(const CUtensorMap (&)[6], const BwdArgs&, cudaStream_t);
-extern template int launch<128, true>(const CUtensorMap (&)[6], const BwdArgs&, cudaStream_t);
+extern template int launch<64, false>(const CUtensorMap (&)[8], const BwdArgs&, cudaStream_t);
+extern template int launch<64, true>(const CUtensorMap (&)[8], const BwdArgs&, cudaStream_t);
+extern template int launch<128, false>(const CUtensorMap (&)[8], const BwdArgs&, cudaStream_t);
+extern template int launch<128, true>(const CUtensorMap (&)[8], const BwdArgs&, cudaStream_t);
 
 }  // namespace bwd
 
@@ -22,13 +22,15 @@ int dense_bwd_shares(const DenseDims& a) {
 int launch_dense_bwd(const DenseDims& a, const DenseTensor& q, const DenseTensor& k, const DenseTensor& v,
                      const DenseTensor& dout, const DenseTensor& dk, const DenseTensor& dv, const DenseBwdBuf& w,
                      cudaStream_t st) {
-  CUtensorMap m[6];
+  CUtensorMap m[8];
   if (make_tmap_dense(&m[0], q, a.d, a.Sq, a.Hq, a.B, 1, bwd::kQTile) ||
       make_tmap_dense(&m[1], k, a.d, a.Skv, a.Hkv, a.B, 1, kKeyTile) ||
       make_tmap_dense(&m[2], v, a.d, a.Skv, a.Hkv, a.B, 1, kKeyTile) ||
       make_tmap_dense(&m[3], dout, a.d, a.Sq, a.Hq, a.B, 1, bwd::kQTile) ||
       make_tmap_f32_3d(&m[4], w.dqacc, a.d, a.Sq, a.B * a.Hq, 32, bwd::kQTile) ||
-      make_tmap_stats(&m[5], w.stats, a.Sq, a.B * a.Hq, bwd::kQTile))
+      make_tmap_stats(&m[5], w.stats, a.Sq, a.B * a.Hq, bwd::kQTile) ||
+      make_tmap_dense(&m[6], dk, a.d, a.Skv, a.Hkv, a.B, 1, kKeyTile) ||
+      make_tmap_dense(&m[7], dv, a.d, a.Skv, a.Hkv, a.B, 1, kKeyTile))
     return LH_ERR_CUDA;
   bwd::BwdArgs p;
   p.a = a;
@@ -37,10 +39,6 @@ int launch_dense_bwd(const DenseDims& a, const DenseTensor& q, const DenseTensor
   p.head_fast = p.nkt < bwd::kHeadFastBelow;
   p.w = w;
   if (p.heads == a.G) p.w.dkv = nullptr;
-  p.dk = const_cast<void*>(dk.p);
-  p.dv = const_cast<void*>(dv.p);
-  p.dks = dk.st;
-  p.dvs = dv.st;
   KernelTimer timer("dense_bwd", st);
   return a.d == 64 ? (a.f16 ? bwd::launch<64, true>(m, p, st) : bwd::launch<64, false>(m, p, st))
                    : (a.f16 ? bwd::launch<128, true>(m, p, st) : bwd::launch<128, false>(m, p, st));

@@ -68,8 +68,6 @@ struct BwdArgs {
   DenseDims a;
   int nkt, heads, head_fast;  // key tiles; query heads of one block (a divisor of G)
   DenseBwdBuf w;
-  void *dk, *dv;
-  Strides dks, dvs;
 };
 
 template <int D, bool F16, bool CAP, int BIAS>
@@ -77,6 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     dense_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                      const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmST,
+                     const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
                      const __grid_constant__ BwdArgs p) {
   using Lay = BwdLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -468,33 +467,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t tacc = hc == 0 ? tDV : tDK;
       const float f = hc == 0 ? (F16 ? 1.f / kShift16 : 1.f) : q_out;
-      const Strides& st = hc == 0 ? p.dvs : p.dks;
-      uint16_t* dst = static_cast<uint16_t*>(hc == 0 ? p.dv : p.dk) + b * st.b + kvh * st.h + key * st.s;
-      // with the query heads shared out, fp32 sums [share][dV, dK][B Hkv][Skv][d], added by another kernel
-      float* part = p.w.dkv ? p.w.dkv + ((((int64_t)blockIdx.z * 2 + hc) * a.B * a.Hkv + bh) * a.Skv + key) * D : nullptr;
-      const RowStage stage{smem + (hc == 0 ? Lay::K : Lay::V) + quarter * (Lay::KT / 4)};  // (K and V are consumed)
-      const uint32_t rows = __ballot_sync(0xffffffffu, key < a.Skv);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        float v[32];
+      uint8_t* tile = smem + (hc == 0 ? Lay::K : Lay::V);  // (K and V are consumed)
+      auto result = [&](int c, float (&v)[32]) {
         if (nit > 0) {
           tmem_ld32(tacc + lane_base + c * 32, v);
           tmem_ld_wait();
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = nit > 0 ? v[e] * f : 0.f;
-        if (part) {
+      };
+      if (p.w.dkv) {  // query heads shared out: fp32 sums [share][dV, dK][B Hkv][Skv][d], added by another kernel
+        float* part = p.w.dkv + ((((int64_t)blockIdx.z * 2 + hc) * a.B * a.Hkv + bh) * a.Skv + key) * D;
+        const RowStage stage{tile + quarter * 4096};
+        const uint32_t rows = __ballot_sync(0xffffffffu, key < a.Skv);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          result(c, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<float4*>(stage.at(lane, e)) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           stage.flush(rows, part + 32 * c, lane);
-        } else {
+        }
+      } else {  // the whole tile in the layout K and V came in, by TMA (rows at or beyond Skv are outside its tensor)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const RowStage stage{tile + (c >> 1) * 16384 + quarter * 4096};
+          float v[32];
+          result(c, v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint4 lo;
             *stage.at(lane, 4 * (c & 1) + e) = round8<F16>(v + 8 * e, &lo);
           }
-          if (c & 1) stage.flush(rows, dst + 32 * (c - 1), lane);
+        }
+        fence_proxy_async_smem();
+        named_barrier_and(3 + hc, 128, true);
+        if (r == 0) {
+          for (int db = 0; db < D / 64; ++db)
+            tma_store_5d(hc == 0 ? &tmDV : &tmDK, smem_u32(tile + db * 16384), db * 64, 0, k0, kvh, b);
+          bulk_commit_group();
+          bulk_wait_group0();
         }
       }
     }
@@ -549,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool F16, bool CAP, int BIAS>
-int launch_t(const CUtensorMap (&m)[6], const BwdArgs& p, cudaStream_t st) {
+int launch_t(const CUtensorMap (&m)[8], const BwdArgs& p, cudaStream_t st) {
   auto kernel = dense_bwd_kernel<D, F16, CAP, BIAS>;
   const int smem = BwdLayout<D>::BYTES + 1024;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared-memory limit is set
@@ -562,12 +575,12 @@ int launch_t(const CUtensorMap (&m)[6], const BwdArgs& p, cudaStream_t st) {
   }
   const int nbh = p.a.B * p.a.Hkv, nz = p.a.G / p.heads;
   const dim3 grid = p.head_fast ? dim3(nbh, p.nkt, nz) : dim3(p.nkt, nbh, nz);
-  kernel<<<grid, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
+  kernel<<<grid, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
   return check_launch();
 }
 // Instantiated for each width and type in a file of its own.
 template <int D, bool F16>
-int launch(const CUtensorMap (&m)[6], const BwdArgs& p, cudaStream_t st) {
+int launch(const CUtensorMap (&m)[8], const BwdArgs& p, cudaStream_t st) {
   const int bias = p.a.slopes ? 1 : p.a.table ? 2 : 0;
   const bool cap = p.a.cap > 0.f;
   if (bias == 0) return cap ? launch_t<D, F16, true, 0>(m, p, st) : launch_t<D, F16, false, 0>(m, p, st);

@@ -3,6 +3,6 @@
 
 namespace lh {
 namespace bwd {
-template int launch<128, false>(const CUtensorMap (&)[6], const BwdArgs&, cudaStream_t);
+template int launch<128, false>(const CUtensorMap (&)[8], const BwdArgs&, cudaStream_t);
 }  // namespace bwd
 }  // namespace lh

@@ -1,13 +1,11 @@
 // dense_fwd.cu — host side of the dense stage's forward: how a call is cut into blocks, and the join of split keys.
-#include <stdlib.h>
 #include "dense_fwd.cuh"
 
 namespace lh {
 namespace fwd {
 
 #define LH_DENSE_FWD(D, F16)                                                                                         \
-  extern template int launch<D, F16>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const FwdArgs&,     \
-                                     const BucketStarts&, int, cudaStream_t);
+  extern template int launch<D, F16>(const FwdMaps&, const FwdArgs&, const BucketStarts&, int, cudaStream_t);
 LH_DENSE_FWD(64, false)
 LH_DENSE_FWD(64, true)
 LH_DENSE_FWD(128, false)
@@ -92,7 +90,6 @@ DenseFwdPlan dense_fwd_plan(const DenseDims& a) {
   const int nk = (a.Skv + kTile - 1) / kTile;
   // Too few blocks for the SMs: as many shares of the keys as fill them once, of four tiles at least.
   f.nsplit = 1;
-  if (getenv("NSPLIT")) { f.nsplit = atoi(getenv("NSPLIT")); return f; }
   if (blocks <= kSms / 2) {
     f.nsplit = (int)(kSms / blocks);
     if (f.nsplit > (nk + 3) / 4) f.nsplit = (nk + 3) / 4;
@@ -105,10 +102,12 @@ int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTens
                      const DenseTensor& v, const DenseTensor& o, const DenseTensor& low, float* lse, const int2* kdoc,
                      float* part_o, float* part_lse, cudaStream_t st) {
   const DenseFwdPlan f = dense_fwd_plan(a);
-  CUtensorMap mq, mk, mv;
-  if (make_tmap_dense(&mq, q, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok) ||
-      make_tmap_dense(&mk, k, a.d, a.Skv, a.Hkv, a.B, 1, kTile) ||
-      make_tmap_dense(&mv, v, a.d, a.Skv, a.Hkv, a.B, 1, kTile))
+  FwdMaps m;
+  if (make_tmap_dense(&m.q, q, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok) ||
+      make_tmap_dense(&m.k, k, a.d, a.Skv, a.Hkv, a.B, 1, kTile) ||
+      make_tmap_dense(&m.v, v, a.d, a.Skv, a.Hkv, a.B, 1, kTile) ||
+      make_tmap_dense(&m.o, o, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok) ||
+      make_tmap_dense(&m.low, low.p ? low : o, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok))
     return LH_ERR_CUDA;
   fwd::FwdArgs p;
   p.a = a;
@@ -145,8 +144,8 @@ int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTens
   int rc;
   {
     KernelTimer timer("dense_fwd", st);
-    rc = a.d == 64 ? (a.f16 ? fwd::launch<64, true>(mq, mk, mv, p, bs, smem, st) : fwd::launch<64, false>(mq, mk, mv, p, bs, smem, st))
-                   : (a.f16 ? fwd::launch<128, true>(mq, mk, mv, p, bs, smem, st) : fwd::launch<128, false>(mq, mk, mv, p, bs, smem, st));
+    rc = a.d == 64 ? (a.f16 ? fwd::launch<64, true>(m, p, bs, smem, st) : fwd::launch<64, false>(m, p, bs, smem, st))
+                   : (a.f16 ? fwd::launch<128, true>(m, p, bs, smem, st) : fwd::launch<128, false>(m, p, bs, smem, st));
   }
   if (rc || f.nsplit == 1) return rc;
   KernelTimer timer("dense_join", st);

@@ -60,6 +60,9 @@ constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
 enum { kBQ = 0, kBFull = 1, kBFree = kBFull + kMaxSlots, kBSF = kBFree + kMaxSlots, kBPF = kBSF + 2, kBOD = kBPF + 4,
        kBDrain = kBOD + 2, kNBar = kBDrain + 2 };
 
+struct FwdMaps {
+  CUtensorMap q, k, v, o, low;
+};
 struct FwdArgs {
   DenseDims a;
   int pack, tok, rep, ntile, npair, nsplit, dual, head_fast, slots;
@@ -74,8 +77,7 @@ struct FwdArgs {
 
 template <int D, bool F16, bool CAP, int BIAS, int REP>
 __global__ void __launch_bounds__(kThreads, 1)
-    dense_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs p,
+    dense_fwd_kernel(const __grid_constant__ FwdMaps m, const __grid_constant__ FwdArgs p,
                      const __grid_constant__ BucketStarts starts) {
   constexpr uint32_t TILE = kTile * D * 2;
   constexpr int ROWS = kTile / REP, CH = 4 / REP;  // rows of a copy of the queries; 32-column runs of a thread
@@ -127,9 +129,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_first = INT32_MAX;
     s_last = -1;
     s_bad = 0;
-    prefetch_tmap(&tmQ);
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
+    prefetch_tmap(&m.q);
+    prefetch_tmap(&m.k);
+    prefetch_tmap(&m.v);
   }
   if (warp == 1) tmem_alloc(smem_u32(&s_tmem), 512);
   if (BIAS == 2)
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < nqt; ++q)
           for (int db = 0; db < D / 64; ++db)
             for (int c = 0; c < REP; ++c)
-              tma_load_5d(sb + q * TILE + db * 16384 + c * ROWS * 128, &tmQ, bar(kBQ), db * 64, 0, tok0(q), hp, b);
+              tma_load_5d(sb + q * TILE + db * 16384 + c * ROWS * 128, &m.q, bar(kBQ), db * 64, 0, tok0(q), hp, b);
       }
       int n = 0;  // loads
       Ring r;
@@ -229,15 +231,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           mbar_arrive_expect_tx(bar(kBFull + slot), TILE);
           for (int db = 0; db < D / 64; ++db)
-            tma_load_5d(sb + p.off_kv + slot * TILE + db * 16384, kv ? &tmV : &tmK, bar(kBFull + slot), db * 64, 0,
+            tma_load_5d(sb + p.off_kv + slot * TILE + db * 16384, kv ? &m.v : &m.k, bar(kBFull + slot), db * 64, 0,
                         t * kTile, kvh, b);
           ++n;
           r.step(p.slots);
         }
       if (!ok) {  // drain the copies this thread issued before leaving
         if (e == 0) mbar_wait_teardown(bar(kBQ), 0);
-        for (int m = n > p.slots ? n - p.slots : 0; m < n; ++m)
-          mbar_wait_teardown(bar(kBFull + e * p.slots + m % p.slots), (m / p.slots) & 1);
+        for (int i = n > p.slots ? n - p.slots : 0; i < n; ++i)
+          mbar_wait_teardown(bar(kBFull + e * p.slots + i % p.slots), (i / p.slots) & 1);
       }
     }
   } else {
@@ -665,18 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           ok = named_barrier_and(1 + q, kTile, ok);  // the group's flags of tiles with values that are not finite
         }
-        if (ok && active && (q == 0 || !p.dual)) {
+        if (ok && (q == 0 || !p.dual)) {
           const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
           const int64_t ri = ((int64_t)b * a.Hq + h) * a.Sq + tk;
           const bool use0 = cnt > 0 && inv != 0.f, use1 = p.dual && a1 != 0.f && inv != 0.f;
-          const uint32_t rows = __ballot_sync(0xffffffffu, valid);
-          const RowStage stage{smem + (p.dual ? 0 : q) * TILE + quarter * 4096};  // (the queries are consumed)
-          uint16_t *orow = out(p.o, h, tk), *lrow = out(p.low, h, tk);
-          float* prow = part ? p.part_o + (pbase + ri) * D : nullptr;
-          uint4 lo[8];
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
+          // features [32 c, 32 c + 32) of this row
+          auto result = [&](int c, float (&o)[32]) {
             if (cnt > 0) {
               tmem_ld32(tO + c * 32, o);
               tmem_ld_wait();
@@ -688,23 +684,66 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 32; ++i) o[i] = fmaf(so[(c * 32 + i) * kTile + row], a1 * inv, o[i]);
             }
             if (valid) add_bad(jlast, mydoc, c * 32, 32, o);
-            if (part) {
+          };
+          uint8_t* tile = smem + (p.dual ? 0 : q) * TILE;  // the queries' place, consumed
+          if (part) {
+            const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+            const RowStage stage{tile + quarter * 4096};
+            float* prow = p.part_o + (pbase + ri) * D;
+            if (active) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4*>(stage.at(lane, i)) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              stage.flush(rows, prow + 32 * c, lane);
-            } else {
+              for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                result(c, o);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) *stage.at(lane, 4 * (c & 1) + i) = round8<F16>(o + 8 * i, lo + 4 * (c & 1) + i);
-              if (c & 1) {
-                stage.flush(rows, orow + 32 * (c - 1), lane);
-                if (p.low.p) {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) *stage.at(lane, i) = lo[i];
-                  stage.flush(rows, lrow + 32 * (c - 1), lane);
-                }
+                for (int i = 0; i < 8; ++i)
+                  *reinterpret_cast<float4*>(stage.at(lane, i)) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                stage.flush(rows, prow + 32 * c, lane);
               }
             }
+          } else {
+            // 64 features of all rows at a time, in the layout the queries came in, leave by one TMA store (rows at or
+            // beyond Sq are outside its tensor); at d = 128 the low halves have the tile's second block, else its turn
+            const RowStage stage{tile + quarter * 4096}, stage2{tile + (D == 128 ? 16384 : 0) + quarter * 4096};
+            const bool chief = row == 0;
+            auto send = [&](const CUtensorMap* map, const RowStage& from, int half) {
+              tma_store_5d(map, smem_u32(from.buf), half * 64, 0, tok0(q), hp, b);
+              bulk_commit_group();
+            };
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+              uint4 lo[8];
+              if (active) {
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                  float o[32];
+                  result(2 * half + cc, o);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    *stage.at(lane, 4 * cc + i) = round8<F16>(o + 8 * i, lo + 4 * cc + i);
+                    if (D == 128 && p.low.p) *stage2.at(lane, 4 * cc + i) = lo[4 * cc + i];
+                  }
+                }
+              }
+              fence_proxy_async_smem();
+              named_barrier_and(1 + q, kTile, true);
+              if (chief) {
+                send(&m.o, stage, half);
+                if (D == 128 && p.low.p) send(&m.low, stage2, half);
+              }
+              if (half + 1 < D / 64 || (D == 64 && p.low.p)) {  // the block is written again
+                if (chief) bulk_wait_group_read0();
+                named_barrier_and(1 + q, kTile, true);
+              }
+              if (D == 64 && p.low.p) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) *stage2.at(lane, i) = lo[i];
+                fence_proxy_async_smem();
+                named_barrier_and(1 + q, kTile, true);
+                if (chief) send(&m.low, stage2, half);
+              }
+            }
+            if (chief) bulk_wait_group0();
           }
           if (valid) stats(ri, m_run, l_run);
         }
@@ -778,8 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool F16, bool CAP, int BIAS, int REP>
-int launch_r(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const FwdArgs& p,
-             const BucketStarts& bs, int smem, cudaStream_t st) {
+int launch_r(const FwdMaps& m, const FwdArgs& p, const BucketStarts& bs, int smem, cudaStream_t st) {
   auto kernel = dense_fwd_kernel<D, F16, CAP, BIAS, REP>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared-memory limit is set
   int dev = 0;
@@ -791,27 +829,25 @@ int launch_r(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv
   }
   const int nbh = p.a.B * (p.a.Hq / p.pack);
   const dim3 grid = p.head_fast ? dim3(nbh, p.npair, p.nsplit) : dim3(p.npair, nbh, p.nsplit);
-  kernel<<<grid, kThreads, smem, st>>>(mq, mk, mv, p, bs);
+  kernel<<<grid, kThreads, smem, st>>>(m, p, bs);
   return check_launch();
 }
 template <int D, bool F16, bool CAP, int BIAS>
-int launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const FwdArgs& p,
-             const BucketStarts& bs, int smem, cudaStream_t st) {
-  return p.rep == 4 ? launch_r<D, F16, CAP, BIAS, 4>(mq, mk, mv, p, bs, smem, st)
-                    : launch_r<D, F16, CAP, BIAS, 1>(mq, mk, mv, p, bs, smem, st);
+int launch_t(const FwdMaps& m, const FwdArgs& p, const BucketStarts& bs, int smem, cudaStream_t st) {
+  return p.rep == 4 ? launch_r<D, F16, CAP, BIAS, 4>(m, p, bs, smem, st)
+                    : launch_r<D, F16, CAP, BIAS, 1>(m, p, bs, smem, st);
 }
 // Instantiated for each width and type in a file of its own.
 template <int D, bool F16>
-int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const FwdArgs& p,
-             const BucketStarts& bs, int smem, cudaStream_t st) {
+int launch(const FwdMaps& m, const FwdArgs& p, const BucketStarts& bs, int smem, cudaStream_t st) {
   const int bias = p.a.slopes ? 1 : p.a.table ? 2 : 0;
   const bool cap = p.a.cap > 0.f;
-  if (bias == 0) return cap ? launch_t<D, F16, true, 0>(mq, mk, mv, p, bs, smem, st)
-                            : launch_t<D, F16, false, 0>(mq, mk, mv, p, bs, smem, st);
-  if (bias == 1) return cap ? launch_t<D, F16, true, 1>(mq, mk, mv, p, bs, smem, st)
-                            : launch_t<D, F16, false, 1>(mq, mk, mv, p, bs, smem, st);
-  return cap ? launch_t<D, F16, true, 2>(mq, mk, mv, p, bs, smem, st)
-             : launch_t<D, F16, false, 2>(mq, mk, mv, p, bs, smem, st);
+  if (bias == 0) return cap ? launch_t<D, F16, true, 0>(m, p, bs, smem, st)
+                            : launch_t<D, F16, false, 0>(m, p, bs, smem, st);
+  if (bias == 1) return cap ? launch_t<D, F16, true, 1>(m, p, bs, smem, st)
+                            : launch_t<D, F16, false, 1>(m, p, bs, smem, st);
+  return cap ? launch_t<D, F16, true, 2>(m, p, bs, smem, st)
+             : launch_t<D, F16, false, 2>(m, p, bs, smem, st);
 }
 
 }  // namespace fwd

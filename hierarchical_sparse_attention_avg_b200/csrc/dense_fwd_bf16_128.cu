@@ -3,7 +3,6 @@
 
 namespace lh {
 namespace fwd {
-template int launch<128, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const FwdArgs&, const BucketStarts&, int,
-                 cudaStream_t);
+template int launch<128, false>(const FwdMaps&, const FwdArgs&, const BucketStarts&, int, cudaStream_t);
 }  // namespace fwd
 }  // namespace lh

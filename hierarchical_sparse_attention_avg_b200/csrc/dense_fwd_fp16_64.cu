@@ -3,7 +3,6 @@
 
 namespace lh {
 namespace fwd {
-template int launch<64, true>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const FwdArgs&, const BucketStarts&, int,
-                 cudaStream_t);
+template int launch<64, true>(const FwdMaps&, const FwdArgs&, const BucketStarts&, int, cudaStream_t);
 }  // namespace fwd
 }  // namespace lh
