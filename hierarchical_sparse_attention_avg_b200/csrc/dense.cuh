@@ -107,8 +107,8 @@ __device__ __forceinline__ uint32_t same_doc(int other, int mine) {
 // tanh, |error| <= about 2e-7 every way (the hardware's tanh has 5e-4: times a cap of 50 a score off by 0.02, more than
 // the operands' own rounding gives).  Where a warp's arguments are all small (scores below the cap, nearly always), an odd
 // polynomial on pairs, x p(x^2) with p fitted to tanh(x) / x for the least |error| of tanh (weighted least squares, the
-// weights raised where the error was large): on [0, 1/2] with 4 coefficients 1.6e-7, on [0, 1] with 7 coefficients 0.9e-7;
-// 6 or 9 packed FMAs a pair, against two exponentials and two reciprocals, whose pipe the softmax itself fills.
+// weights raised where the error was large): on [0, 1/2] with 4 coefficients 1.6e-7, on [0, 5/4] with 8 coefficients 1.2e-7;
+// 6 or 10 packed FMAs a pair, against two exponentials and two reciprocals, whose pipe the softmax itself fills.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -119,17 +119,17 @@ __device__ __forceinline__ float tanh_any(float x) {
 }
 template <bool Half>
 struct TanhPoly {  // f * tanh
-  static constexpr int N = Half ? 4 : 7;
+  static constexpr int N = Half ? 4 : 8;
   uint64_t c[N];
   __device__ __forceinline__ explicit TanhPoly(float f) {
     const float k4[4] = {0.999997677f, -0.33320657f, 0.131451624f, -0.0433729225f};
-    const float k7[7] = {0.999999693f, -0.333321293f, 0.133195837f, -0.053265835f, 0.0199732811f, -0.00595127819f,
-                         0.000963771153f};
+    const float k8[8] = {0.999999512f, -0.333317329f, 0.133179241f, -0.0532919123f, 0.0202494413f, -0.00654016651f,
+                         0.00147954026f, -0.000164161214f};
 #pragma unroll
-    for (int i = 0; i < N; ++i) c[i] = f2pack((Half ? k4[i % 4] : k7[i]) * f, (Half ? k4[i % 4] : k7[i]) * f);
+    for (int i = 0; i < N; ++i) c[i] = f2pack((Half ? k4[i % 4] : k8[i]) * f, (Half ? k4[i % 4] : k8[i]) * f);
   }
 };
-// f tanh(in v) of 32 values, all of magnitude <= 1/2 (Half) or 1 after the scaling.
+// f tanh(in v) of 32 values, all of magnitude <= 1/2 (Half) or 5/4 after the scaling.
 template <bool Half>
 __device__ __forceinline__ void tanh32(float (&v)[32], float in, float f) {
   const TanhPoly<Half> poly(f);

@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float big = absmax32(sv, 0.f) * cap_in;
           if (__all_sync(0xffffffffu, big <= 0.5f)) {
             tanh32<true>(sv, cap_in, 1.f);
-          } else if (__all_sync(0xffffffffu, big <= 1.f)) {
+          } else if (__all_sync(0xffffffffu, big <= 1.25f)) {
             tanh32<false>(sv, cap_in, 1.f);
           } else {
 #pragma unroll

@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < CH; ++c) big = absmax32(s[c], big);
             }
             big *= cap_in;
-            if (REP == 1 && __all_sync(0xffffffffu, !valid || big <= 1.f)) {
+            if (REP == 1 && __all_sync(0xffffffffu, !valid || big <= 1.25f)) {
 #pragma unroll
               for (int c = 0; c < CH; ++c) tanh32<false>(s[c], cap_in, mul0);
               mul = 1.f;
