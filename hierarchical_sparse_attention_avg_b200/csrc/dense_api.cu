@@ -77,7 +77,7 @@ int make_dense(const lh_attn_params* P, const lh_attn_mods* M, DenseDims* a, Buc
       ((uintptr_t)M->table & 1u))
     return LH_ERR_INVALID_ARG;
   a->slopes = M->slopes; a->table = M->table; a->docs = M->docs; a->prefix = M->prefix; a->kv_len = M->kv_len;
-  return device_status(&a->status);
+  return LH_OK;
 }
 
 // Checks a tensor and takes its strides (a dimension of one gets those of a contiguous tensor).
@@ -172,6 +172,7 @@ int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_ten
     return LH_ERR_INVALID_ARG;
   const DenseWs w = dense_ws(a);
   if (!aligned16(ws) || ws_bytes < w.fwd_total) return ws ? LH_ERR_WORKSPACE : LH_ERR_INVALID_ARG;
+  LH_TRY(device_status(&a.status));
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   cudaStream_t st = (cudaStream_t)stream;
   int2* kdoc = reinterpret_cast<int2*>(wsb + w.kdoc);
@@ -197,6 +198,7 @@ int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_te
     return LH_ERR_INVALID_ARG;
   const DenseWs w = dense_ws(a);
   if (!aligned16(ws) || ws_bytes < w.bwd_total) return ws ? LH_ERR_WORKSPACE : LH_ERR_INVALID_ARG;
+  LH_TRY(device_status(&a.status));
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   cudaStream_t st = (cudaStream_t)stream;
   DenseBwdBuf buf;

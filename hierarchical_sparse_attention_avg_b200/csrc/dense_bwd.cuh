@@ -179,11 +179,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_3d(sb + Lay::STAT + s * Lay::ST, &tmST, bar(Lay::B_QF + s), row, b * a.Hq + h, 0);  // both planes
         issued = it + 1;
       }
-      if (!ok) {
-        mbar_wait_teardown(bar(Lay::B_KV), 0);
-        for (int it = issued >= kStages ? issued - kStages : 0; it < issued; ++it)
-          mbar_wait_teardown(bar(Lay::B_QF + it % kStages), (it / kStages) & 1);
-      }
+      // every copy has landed before the block lets go of its memory, whoever gave up
+      mbar_wait_teardown(bar(Lay::B_KV), 0);
+      for (int it = issued >= kStages ? issued - kStages : 0; it < issued; ++it)
+        mbar_wait_teardown(bar(Lay::B_QF + it % kStages), (it / kStages) & 1);
     }
    } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (the whole warp, one lane issuing)

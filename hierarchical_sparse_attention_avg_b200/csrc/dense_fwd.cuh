@@ -51,7 +51,7 @@ constexpr int kSms = 148;
 constexpr uint32_t kSmemLimit = 226 * 1024;  // dynamic shared memory of a block, beside at most 1 KB of static
 
 // flag byte of a key tile: bit q visible to stream q, 2 + q some pair masked, 4 + q distances of several buckets (or
-// signs, with slopes), 6 + q some value row not finite (set by the softmax threads)
+// signs, with slopes), 6 a value row that is not finite was cleared
 constexpr int kSees = 1, kMasked = 4, kNear = 16, kBad = 64;
 
 // Registers a thread: 128 * 56 + 256 * 224 = 384 * 168, what the block is launched with.
@@ -236,11 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n;
           r.step(p.slots);
         }
-      if (!ok) {  // drain the copies this thread issued before leaving
-        if (e == 0) mbar_wait_teardown(bar(kBQ), 0);
-        for (int i = n > p.slots ? n - p.slots : 0; i < n; ++i)
-          mbar_wait_teardown(bar(kBFull + e * p.slots + i % p.slots), (i / p.slots) & 1);
-      }
+      // every copy has landed before the block lets go of its memory, whoever gave up
+      if (e == 0) mbar_wait_teardown(bar(kBQ), 0);
+      for (int i = n > p.slots ? n - p.slots : 0; i < n; ++i)
+        mbar_wait_teardown(bar(kBFull + e * p.slots + i % p.slots), (i / p.slots) & 1);
     }
   } else {
     // ---------------------------------------------------------------- MMA issuers (whole warps, one lane issuing)
@@ -432,14 +431,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
               *reinterpret_cast<uint4*>(vr + (i >> 3) * 16384 + (((i + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          } else if (bad) {
+          } else if (bad) {  // (the flag first: the other stream's product may find the cleared row)
+            atomicOr(reinterpret_cast<unsigned int*>(flags) + ((t - ks) >> 2), (unsigned)kBad << (8 * ((t - ks) & 3)));
+            *static_cast<volatile int*>(&s_bad) = 1;
+            __threadfence_block();
 #pragma unroll 1
             for (int i = 0; i < D; ++i) {
               unsigned short* e = reinterpret_cast<unsigned short*>(vr + (i >> 6) * 16384) + (i & 63);
               if (nonfinite2<F16>(*e)) *e = 0;
             }
-            atomicOr(reinterpret_cast<unsigned int*>(flags) + ((t - ks) >> 2), (unsigned)(kBad << q) << (8 * ((t - ks) & 3)));
-            s_bad = 1;
           }
           fence_proxy_async_smem();
         }
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!*static_cast<volatile int*>(&s_bad)) return;
 #pragma unroll 1
         for (int t = first; t <= last; ++t) {
-          if (!(flags[t - ks] & (p.dual ? 3 * kBad : kBad << q))) continue;
+          if (!(flags[t - ks] & kBad)) continue;
 #pragma unroll 1
           for (int j = t * kTile; j < min((t + 1) * kTile, jl + 1); ++j) {
             if (a.docs && (doc < 0 || doc_at(a, b, j, len) != doc)) continue;
