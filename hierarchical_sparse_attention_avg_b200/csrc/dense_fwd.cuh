@@ -29,8 +29,10 @@
 // in shared memory before the product (dead rows for good; others are added to the rows that see them at the end).
 //
 // Precision: Q, K, V enter as they are, scores and statistics fp32; the probabilities are rounded once to the operands'
-// type (2^-9 bf16, 2^-12 fp16 relative) as both operands of one tensor-core product must share it, and lie in
-// [0, 2^8] against a reference maximum that moves only when exceeded by more than 2^8.
+// type (2^-9 bf16, 2^-12 fp16 relative), as both operands of one tensor-core product must share it.  They are taken against
+// the running maximum itself, so that a row's largest one is 1 and exact: with a maximum that only moves when exceeded by
+// 2^8 the accumulator is rescaled more rarely (269 us instead of 275 at 16 heads of 8,192 causal keys), but <dO, O>, which
+// the backward subtracts from nearly equal numbers, then makes bf16 dQ and dK 2.8e-3 off instead of 2.4e-3.
 #pragma once
 
 #include <atomic>
@@ -45,7 +47,6 @@ constexpr int kTile = 128;
 constexpr int kMaxSlots = 12;  // key and value tiles in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;
 constexpr int kHeadFastBelow = 512;  // as in the gathered attention: heads fastest, heaviest tiles first, below this
 constexpr int kSms = 148;
 constexpr uint32_t kSmemLimit = 226 * 1024;  // dynamic shared memory of a block, beside at most 1 KB of static
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mx = fmaf(fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                       fmaxf(mx8[6], mx8[7])), mul, cadd);
           float alpha = 1.0f;
-          const bool move = __any_sync(0xffffffffu, valid && mx > m_run + kSlack);
+          const bool move = __any_sync(0xffffffffu, valid && mx > m_run);
           if (move) {
             const float m_new = fmaxf(m_run, mx);
             alpha = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
