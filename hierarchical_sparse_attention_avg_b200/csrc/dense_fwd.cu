@@ -12,14 +12,14 @@ LH_DENSE_FWD(128, false)
 LH_DENSE_FWD(128, true)
 #undef LH_DENSE_FWD
 
-// Joins the splits of a row: one block per row, its warps over the splits, then over shared memory.  Reads
-// nsplit (d + 1) floats a row; latency-bound (a few rows per SM).
-template <int D, bool F16>
+// Joins the splits of a row: W warps a row over its splits (one where they are few, so that many rows are in flight), then
+// over shared memory.  Reads nsplit (d + 1) floats a row; latency-bound (tens of rows per SM).
+template <int D, bool F16, int W>
 __global__ void __launch_bounds__(128) join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
                                                    DenseTensor o, DenseTensor low, float* __restrict__ lse, int nsplit,
                                                    int64_t rows, int Hq, int Sq) {
-  const int64_t row = blockIdx.x;
-  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int slot = threadIdx.x / (32 * W), w = threadIdx.x / 32 % W, lane = threadIdx.x % 32;
+  const int64_t row = min((int64_t)blockIdx.x * (4 / W) + slot, rows - 1);  // (a last block's spare warps repeat a row)
   constexpr int E = D / 32;
   __shared__ float s_acc[4][D], s_l[4];
   float m = -INFINITY;
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(128) join_kernel(const float* __restrict__ par
   const float mm = m == -INFINITY ? 0.f : m;
   float acc[E] = {}, l = 0.f;
 #pragma unroll 4
-  for (int s = w; s < nsplit; s += 4) {
+  for (int s = w; s < nsplit; s += W) {
     const float ls = part_lse[s * rows + row], c = ex2(ls - mm);
     const float* src = part_o + (s * rows + row) * D + lane * E;
     float v[E];
@@ -42,25 +42,32 @@ __global__ void __launch_bounds__(128) join_kernel(const float* __restrict__ par
     }
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i) s_acc[w][lane * E + i] = acc[i];
-  if (lane == 0) s_l[w] = l;
+  for (int i = 0; i < E; ++i) s_acc[slot * W + w][lane * E + i] = acc[i];
+  if (lane == 0) s_l[slot * W + w] = l;
   __syncthreads();
-  const float lt = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]), inv = lt == 0.f ? 0.f : 1.0f / lt;
+  float lt = 0.f;
+#pragma unroll
+  for (int e = 0; e < W; ++e) lt += s_l[slot * W + e];
+  const float inv = lt == 0.f ? 0.f : 1.0f / lt;
   const int64_t tk = row % Sq, bh = row / Sq, h = bh % Hq, b = bh / Hq;
   auto at = [&](const DenseTensor& t) {
     return static_cast<uint16_t*>(const_cast<void*>(t.p)) + b * t.st.b + h * t.st.h + tk * t.st.s;
   };
-  const int i = threadIdx.x * 8;
+  const int i = (threadIdx.x % (32 * W)) * 8;
   if (i < D) {
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = ((s_acc[0][i + e] + s_acc[1][i + e]) + (s_acc[2][i + e] + s_acc[3][i + e])) * inv;
+    for (int e = 0; e < 8; ++e) {
+      float x = 0.f;
+#pragma unroll
+      for (int u = 0; u < W; ++u) x += s_acc[slot * W + u][i + e];
+      v[e] = x * inv;
+    }
     uint4 lo;
     st16(at(o) + i, round8<F16>(v, &lo));
     if (low.p) st16(at(low) + i, lo);
   }
-  if (threadIdx.x == 0) lse[row] = lt == 0.f ? -INFINITY : (m + __log2f(lt)) * kLn2;
+  if (threadIdx.x % (32 * W) == 0) lse[row] = lt == 0.f ? -INFINITY : (m + __log2f(lt)) * kLn2;
 }
 
 }  // namespace fwd
@@ -105,9 +112,13 @@ int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTens
   FwdMaps m;
   if (make_tmap_dense(&m.q, q, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok) ||
       make_tmap_dense(&m.k, k, a.d, a.Skv, a.Hkv, a.B, 1, kTile) ||
-      make_tmap_dense(&m.v, v, a.d, a.Skv, a.Hkv, a.B, 1, kTile) ||
-      make_tmap_dense(&m.o, o, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok) ||
-      make_tmap_dense(&m.low, low.p ? low : o, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok))
+      make_tmap_dense(&m.v, v, a.d, a.Skv, a.Hkv, a.B, 1, kTile))
+    return LH_ERR_CUDA;
+  // whole result tiles leave by TMA (few rows, and the parts of split keys, by plain stores: the maps are not used)
+  m.o = m.low = m.q;
+  if (f.rep == 1 && f.nsplit == 1 &&
+      (make_tmap_dense(&m.o, o, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok) ||
+       (low.p && make_tmap_dense(&m.low, low, a.d, a.Sq, a.Hq, a.B, f.pack, f.tok))))
     return LH_ERR_CUDA;
   fwd::FwdArgs p;
   p.a = a;
@@ -150,9 +161,13 @@ int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTens
   if (rc || f.nsplit == 1) return rc;
   KernelTimer timer("dense_join", st);
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
-  auto join = a.d == 64 ? (a.f16 ? join_kernel<64, true> : join_kernel<64, false>)
-                        : (a.f16 ? join_kernel<128, true> : join_kernel<128, false>);
-  join<<<(unsigned)rows, 128, 0, st>>>(part_o, part_lse, o, low, lse, f.nsplit, rows, a.Hq, a.Sq);
+  const bool few = f.nsplit <= 8;
+  auto join = a.d == 64 ? (a.f16 ? (few ? join_kernel<64, true, 1> : join_kernel<64, true, 4>)
+                                 : (few ? join_kernel<64, false, 1> : join_kernel<64, false, 4>))
+                        : (a.f16 ? (few ? join_kernel<128, true, 1> : join_kernel<128, true, 4>)
+                                 : (few ? join_kernel<128, false, 1> : join_kernel<128, false, 4>));
+  const int64_t grid = few ? (rows + 3) / 4 : rows;
+  join<<<(unsigned)grid, 128, 0, st>>>(part_o, part_lse, o, low, lse, f.nsplit, rows, a.Hq, a.Sq);
   return check_launch();
 }
 

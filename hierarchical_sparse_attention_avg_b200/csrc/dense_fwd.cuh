@@ -286,27 +286,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.dual) {  // an issuer per stream: one alone would be busy for longer than the tensor core
         const int mask = 1 << me, s0 = me * p.slots;
         int t = next(last + 1, mask);
-        for (int n = 0; t >= first && ok; ++n) {
-          if (n == 0) {
-            ok = wait(kBFull + s0 + r.s, r.ph);
-            if (!ok) break;
+        if (ok && t >= first) {
+          ok = wait(kBFull + s0, 0);
+          if (ok) {
             tc_fence_after();
-            scores(me, s0 + r.s);
-            umma_commit_by(leader, bar(kBFree + s0 + r.s));
+            scores(me, s0);
+            umma_commit_by(leader, bar(kBFree + s0));
             r.step(p.slots);
           }
-          ok = wait(kBFull + s0 + r.s, r.ph) && values(me, s0 + r.s, n > 0, n & 1);
-          if (!ok) break;
-          umma_commit_by(leader, bar(kBFree + s0 + r.s));
+        }
+        for (int n = 0; t >= first && ok; ++n) {
+          // while the softmax works: the tile's values, and the next tile's keys
+          const int sv = s0 + r.s, tn = next(t, mask);
+          ok = wait(kBFull + sv, r.ph);
           r.step(p.slots);
-          t = next(t, mask);
-          if (t < first) break;
-          ok = wait(kBFull + s0 + r.s, r.ph);
+          const int sk = s0 + r.s;
+          if (ok && tn >= first) ok = wait(kBFull + sk, r.ph);
+          if (ok) ok = values(me, sv, n > 0, n & 1);
           if (!ok) break;
-          tc_fence_after();
-          scores(me, s0 + r.s);
-          umma_commit_by(leader, bar(kBFree + s0 + r.s));
-          r.step(p.slots);
+          if (tn >= first) {
+            scores(me, sk);
+            umma_commit_by(leader, bar(kBFree + sv));
+            umma_commit_by(leader, bar(kBFree + sk));
+            r.step(p.slots);
+          }
+          t = tn;
         }
         umma_commit_by(leader, bar(kBOD + me));
       } else {
@@ -328,21 +332,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int sv = r.s;
           ok = wait(kBFull + sv, r.ph);
           r.step(p.slots);
-          bool k_here = false;
+          if (ok && fa) ok = wait(kBFull + r.s, r.ph);  // the next keys too, while the softmax works
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             if (ok && (f >> q & 1)) {
               ok = values(q, sv, cnt[q] > 0, cnt[q] & 1);
               ++cnt[q];
             }
-            if (ok && (fa >> q & 1)) {
-              if (!k_here) ok = wait(kBFull + r.s, r.ph);
-              k_here = true;
-              if (ok) {
-                tc_fence_after();
-                scores(q, r.s);
-              }
-            }
+            if (ok && (fa >> q & 1)) scores(q, r.s);
           }
           if (!ok) break;
           umma_commit_by(leader, bar(kBFree + sv));

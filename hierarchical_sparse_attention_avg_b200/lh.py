@@ -549,7 +549,7 @@ def _rows(t, shape, dtype, device, name) -> bytes:
     if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     sb, sh, ss, sd = t.stride()
-    if sd != 1 or sb & 7 or sh & 7 or ss & 7 or sb <= 0 or sh <= 0 or ss <= 0:
+    if sd != 1 or (sb | sh | ss) & 7 or sb <= 0 or sh <= 0 or ss <= 0:
         B, H, S, d = shape  # (a dimension of one may have any stride)
         if (sd != 1 and d > 1) or any(n > 1 and (x <= 0 or x & 7) for n, x in ((B, sb), (H, sh), (S, ss))):
             raise ValueError(f"{name}: features must be contiguous and the other strides positive multiples of 8, got "
@@ -577,21 +577,23 @@ def _attn_ws(P: AttnParams, ws, dev, backward, where):
         raise ValueError(f"{where}: expected CUDA tensors")
     if ws is None:
         return new_attn_workspace(P, dev, backward)
-    if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+    if ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous uint8 tensor on {dev}")
     return ws
 
 
+# the current stream's handle without a Stream object around it (these calls are as short as a few microseconds)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _on_device(dev, fn, *args) -> int:
     """The call with the tensors' device current, on its current stream."""
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, _raw_stream(dev.index))
+    index = dev.index
+    if index == torch.cuda.current_device():
+        return fn(*args, _raw_stream(index))
     with torch.cuda.device(dev):
-        return fn(*args, _raw_stream(dev.index))
+        return fn(*args, _raw_stream(index))
 
 
 def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, prefix=None, kv_len=None, o=None,
@@ -600,7 +602,8 @@ def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, 
     ``Sq`` of each entry's ``kv_len`` positions.  ``slopes`` fp32 [Hq]; ``table`` [Hq, buckets] (dtype of q); ``docs``
     int32 [B, Skv]; ``prefix``, ``kv_len`` int32 [B].  ``low`` (like ``o``): receives what o's rounding dropped; handed to
     ``lh_attn_backward`` it makes the gradients about twice as exact."""
-    _check(P._status, "lh_attn_forward")
+    if P._status:
+        _check(P._status, "lh_attn_forward")
     dev = q.device
     ws = _attn_ws(P, ws, dev, False, "lh_attn_forward")
     qs, ks = P._qs, P._ks
@@ -613,7 +616,8 @@ def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, 
                     _rows(q, qs, dt, dev, "q"), _rows(k, ks, dt, dev, "k"), _rows(v, ks, dt, dev, "v"),
                     _rows(o, qs, dt, dev, "o"), None if low is None else _rows(low, qs, dt, dev, "low"),
                     _vec(lse, qs[:3], torch.float32, dev, "lse"), ws.data_ptr(), ws.numel())
-    _check(rc, "lh_attn_forward")
+    if rc:
+        _check(rc, "lh_attn_forward")
     return o, lse
 
 
@@ -621,7 +625,8 @@ def lh_attn_backward(P: AttnParams, q, k, v, o, lse, dout, slopes=None, table=No
                      low=None, dq=None, dk=None, dv=None, dtable=None, ws=None):
     """Gradients ``(dq, dk, dv, dtable)`` of ``lh_attn_forward`` (``dtable`` None without a table); ``o``, ``lse`` and
     ``low`` are its results, the other arguments those it got.  ``ws``: from ``new_attn_workspace(..., backward=True)``."""
-    _check(P._status, "lh_attn_backward")
+    if P._status:
+        _check(P._status, "lh_attn_backward")
     dev = q.device
     ws = _attn_ws(P, ws, dev, True, "lh_attn_backward")
     qs, ks = P._qs, P._ks
