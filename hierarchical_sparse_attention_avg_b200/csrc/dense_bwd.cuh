@@ -155,98 +155,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float q_out = F16 ? a.scale / (fs * kShift16) : a.scale;  // brings dQ and dK to scale
 
   if (warp < 4) {
-   set_regs_dec<kRegsIssue>();
-   if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
-    if (lane == 0 && nit > 0) {
-      bool ok = true;
-      int issued = 0;
-      mbar_arrive_expect_tx(bar(Lay::B_KV), 2 * Lay::KT);
-      for (int db = 0; db < D / 64; ++db) {
-        tma_load_5d(sb + Lay::K + db * 16384, &tmK, bar(Lay::B_KV), db * 64, 0, k0, kvh, b);
-        tma_load_5d(sb + Lay::V + db * 16384, &tmV, bar(Lay::B_KV), db * 64, 0, k0, kvh, b);
-      }
-      for (int it = 0; it < nit && ok; ++it) {
-        const int s = it % kStages;
-        if (it >= kStages) ok = mbar_wait(bar(Lay::B_QE + s), ((it / kStages) - 1) & 1, &s_wait, status);
-        if (!ok) break;
-        const int h = h0 + it / n1, row = (ilo + it % n1) * kQTile;
-        mbar_arrive_expect_tx(bar(Lay::B_QF + s), 2 * Lay::QT + Lay::ST);
+    set_regs_dec<kRegsIssue>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane == 0 && nit > 0) {
+        bool ok = true;
+        int issued = 0;
+        mbar_arrive_expect_tx(bar(Lay::B_KV), 2 * Lay::KT);
         for (int db = 0; db < D / 64; ++db) {
-          tma_load_5d(sb + Lay::Q + s * Lay::QT + db * 8192, &tmQ, bar(Lay::B_QF + s), db * 64, 0, row, h, b);
-          tma_load_5d(sb + Lay::DO + s * Lay::QT + db * 8192, &tmDO, bar(Lay::B_QF + s), db * 64, 0, row, h, b);
+          tma_load_5d(sb + Lay::K + db * 16384, &tmK, bar(Lay::B_KV), db * 64, 0, k0, kvh, b);
+          tma_load_5d(sb + Lay::V + db * 16384, &tmV, bar(Lay::B_KV), db * 64, 0, k0, kvh, b);
         }
-        tma_load_3d(sb + Lay::STAT + s * Lay::ST, &tmST, bar(Lay::B_QF + s), row, b * a.Hq + h, 0);  // both planes
-        issued = it + 1;
+        for (int it = 0; it < nit && ok; ++it) {
+          const int s = it % kStages;
+          if (it >= kStages) ok = mbar_wait(bar(Lay::B_QE + s), ((it / kStages) - 1) & 1, &s_wait, status);
+          if (!ok) break;
+          const int h = h0 + it / n1, row = (ilo + it % n1) * kQTile;
+          mbar_arrive_expect_tx(bar(Lay::B_QF + s), 2 * Lay::QT + Lay::ST);
+          for (int db = 0; db < D / 64; ++db) {
+            tma_load_5d(sb + Lay::Q + s * Lay::QT + db * 8192, &tmQ, bar(Lay::B_QF + s), db * 64, 0, row, h, b);
+            tma_load_5d(sb + Lay::DO + s * Lay::QT + db * 8192, &tmDO, bar(Lay::B_QF + s), db * 64, 0, row, h, b);
+          }
+          tma_load_3d(sb + Lay::STAT + s * Lay::ST, &tmST, bar(Lay::B_QF + s), row, b * a.Hq + h, 0);  // both planes
+          issued = it + 1;
+        }
+        // every copy has landed before the block lets go of its memory, whoever gave up
+        mbar_wait_teardown(bar(Lay::B_KV), 0);
+        for (int it = issued >= kStages ? issued - kStages : 0; it < issued; ++it)
+          mbar_wait_teardown(bar(Lay::B_QF + it % kStages), (it / kStages) & 1);
       }
-      // every copy has landed before the block lets go of its memory, whoever gave up
-      mbar_wait_teardown(bar(Lay::B_KV), 0);
-      for (int it = issued >= kStages ? issued - kStages : 0; it < issued; ++it)
-        mbar_wait_teardown(bar(Lay::B_QF + it % kStages), (it / kStages) & 1);
-    }
-   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer (the whole warp, one lane issuing)
-    if (nit > 0) {
-      constexpr int fmt = F16 ? kFmtF16 : kFmtBF16;
-      constexpr uint32_t idesc_s = idesc_f32acc(fmt, 128, kQTile, 0, 0);   // K-major x K-major
-      constexpr uint32_t idesc_acc = idesc_f32acc(fmt, 128, D, 0, 1);      // K-major x MN-major
-      constexpr uint32_t idesc_dq = idesc_f32acc(fmt, 128, kQTile, 1, 1);  // MN-major x MN-major
-      const uint32_t leader = elect_one();
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t dK = sdesc_sw128(sb + Lay::K, 16, 1024), dV = sdesc_sw128(sb + Lay::V, 16, 1024);
-      const uint64_t dQ = sdesc_sw128(sb + Lay::Q, 16, 1024), dDO = sdesc_sw128(sb + Lay::DO, 16, 1024);
-      const uint64_t tK = sdesc_sw128(sb + Lay::K, 16384, 1024), tDS = sdesc_sw128(sb + Lay::DS, 8192, 1024);  // MN-major
-      const uint64_t tQ = sdesc_sw128(sb + Lay::Q, 8192, 1024), tDO = sdesc_sw128(sb + Lay::DO, 8192, 1024);
-      auto wait = [&](uint32_t i, uint32_t ph) {
-        return __all_sync(0xffffffffu, mbar_wait(bar(i), ph, &s_wait, status)) != 0;
-      };
-      bool ok = wait(Lay::B_KV, 0);
-      auto products = [&](int jt, int s) {  // dV, dK, dQ^T of sub-tile jt, in stage s
-        const int i = jt & 1;
-        if (!wait(Lay::B_DSF + i, (jt >> 1) & 1)) return false;
-        tc_fence_after();
-        const uint64_t bQ = tQ + s * (Lay::QT >> 4), bDO = tDO + s * (Lay::QT >> 4), bDS = tDS + i * (Lay::PT >> 4);
-        const uint32_t aP = tm + 128 * i, aDS = tm + 128 * i + 64;
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer (the whole warp, one lane issuing)
+      if (nit > 0) {
+        constexpr int fmt = F16 ? kFmtF16 : kFmtBF16;
+        constexpr uint32_t idesc_s = idesc_f32acc(fmt, 128, kQTile, 0, 0);   // K-major x K-major
+        constexpr uint32_t idesc_acc = idesc_f32acc(fmt, 128, D, 0, 1);      // K-major x MN-major
+        constexpr uint32_t idesc_dq = idesc_f32acc(fmt, 128, kQTile, 1, 1);  // MN-major x MN-major
+        const uint32_t leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dK = sdesc_sw128(sb + Lay::K, 16, 1024), dV = sdesc_sw128(sb + Lay::V, 16, 1024);
+        const uint64_t dQ = sdesc_sw128(sb + Lay::Q, 16, 1024), dDO = sdesc_sw128(sb + Lay::DO, 16, 1024);
+        const uint64_t tK = sdesc_sw128(sb + Lay::K, 16384, 1024), tDS = sdesc_sw128(sb + Lay::DS, 8192, 1024);  // MN-major
+        const uint64_t tQ = sdesc_sw128(sb + Lay::Q, 8192, 1024), tDO = sdesc_sw128(sb + Lay::DO, 8192, 1024);
+        auto wait = [&](uint32_t i, uint32_t ph) {
+          return __all_sync(0xffffffffu, mbar_wait(bar(i), ph, &s_wait, status)) != 0;
+        };
+        bool ok = wait(Lay::B_KV, 0);
+        auto products = [&](int jt, int s) {  // dV, dK, dQ^T of sub-tile jt, in stage s
+          const int i = jt & 1;
+          if (!wait(Lay::B_DSF + i, (jt >> 1) & 1)) return false;
+          tc_fence_after();
+          const uint64_t bQ = tQ + s * (Lay::QT >> 4), bDO = tDO + s * (Lay::QT >> 4), bDS = tDS + i * (Lay::PT >> 4);
+          const uint32_t aP = tm + 128 * i, aDS = tm + 128 * i + 64;
 #pragma unroll
-        for (int kk = 0; kk < kQTile / 16; ++kk) {  // reduction over the 64 queries
-          const uint32_t acc = (jt > 0 || kk > 0) ? 1u : 0u;
-          const uint32_t pc = (kk >> 1) * 32 + (kk & 1) * 8;  // column half kk/2 packed at 32 (kk/2)
-          umma_ts_by(leader, tm + 256, aP + pc, bDO + kk * (2048 >> 4), idesc_acc, acc);
-          umma_ts_by(leader, tm + 256 + D, aDS + pc, bQ + kk * (2048 >> 4), idesc_acc, acc);
+          for (int kk = 0; kk < kQTile / 16; ++kk) {  // reduction over the 64 queries
+            const uint32_t acc = (jt > 0 || kk > 0) ? 1u : 0u;
+            const uint32_t pc = (kk >> 1) * 32 + (kk & 1) * 8;  // column half kk/2 packed at 32 (kk/2)
+            umma_ts_by(leader, tm + 256, aP + pc, bDO + kk * (2048 >> 4), idesc_acc, acc);
+            umma_ts_by(leader, tm + 256 + D, aDS + pc, bQ + kk * (2048 >> 4), idesc_acc, acc);
+          }
+#pragma unroll
+          for (int kk = 0; kk < kKeyTile / 16; ++kk)  // reduction over the 128 keys
+            umma_ss_by(leader, tm + 128 * i, tK + kk * (2048 >> 4), bDS + kk * (2048 >> 4), idesc_dq, kk > 0 ? 1u : 0u);
+          umma_commit_by(leader, bar(Lay::B_MM + i));
+          umma_commit_by(leader, bar(Lay::B_QE + s));
+          return true;
+        };
+        int s = 0, ph = 0, before = 0;  // stage and phase of sub-tile it, stage of the one before
+        for (int it = 0; it < nit && ok; ++it) {
+          const int i = it & 1;
+          ok = wait(Lay::B_QF + s, ph);
+          // buffer pair i: its dQ^T of sub-tile it-2 has been read out of tensor memory
+          if (ok && it >= 2) ok = wait(Lay::B_DQF + i, ((it >> 1) - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bQ = dQ + s * (Lay::QT >> 4), bDO = dDO + s * (Lay::QT >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4, qo = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
+            umma_ss_by(leader, tm + 128 * i, dK + ko, bQ + qo, idesc_s, kk > 0 ? 1u : 0u);
+            umma_ss_by(leader, tm + 128 * i + 64, dV + ko, bDO + qo, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit_by(leader, bar(Lay::B_SF + i));
+          if (it >= 1) ok = products(it - 1, before);
+          before = s;
+          if (++s == kStages) s = 0, ph ^= 1;
         }
-#pragma unroll
-        for (int kk = 0; kk < kKeyTile / 16; ++kk)  // reduction over the 128 keys
-          umma_ss_by(leader, tm + 128 * i, tK + kk * (2048 >> 4), bDS + kk * (2048 >> 4), idesc_dq, kk > 0 ? 1u : 0u);
-        umma_commit_by(leader, bar(Lay::B_MM + i));
-        umma_commit_by(leader, bar(Lay::B_QE + s));
-        return true;
-      };
-      int s = 0, ph = 0, before = 0;  // stage and phase of sub-tile it, stage of the one before
-      for (int it = 0; it < nit && ok; ++it) {
-        const int i = it & 1;
-        ok = wait(Lay::B_QF + s, ph);
-        // buffer pair i: its dQ^T of sub-tile it-2 has been read out of tensor memory
-        if (ok && it >= 2) ok = wait(Lay::B_DQF + i, ((it >> 1) - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t bQ = dQ + s * (Lay::QT >> 4), bDO = dDO + s * (Lay::QT >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4, qo = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
-          umma_ss_by(leader, tm + 128 * i, dK + ko, bQ + qo, idesc_s, kk > 0 ? 1u : 0u);
-          umma_ss_by(leader, tm + 128 * i + 64, dV + ko, bDO + qo, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        umma_commit_by(leader, bar(Lay::B_SF + i));
-        if (it >= 1) ok = products(it - 1, before);
-        before = s;
-        if (++s == kStages) s = 0, ph ^= 1;
+        if (ok) ok = products(nit - 1, before);
+        umma_commit_by(leader, bar(Lay::B_FIN));  // dV, dK final once every product above has completed
+        umma_commit_by(leader, bar(Lay::B_DRAIN));
+        mbar_wait_teardown(bar(Lay::B_DRAIN), 0);
       }
-      if (ok) ok = products(nit - 1, before);
-      umma_commit_by(leader, bar(Lay::B_FIN));  // dV, dK final once every product above has completed
-      umma_commit_by(leader, bar(Lay::B_DRAIN));
-      mbar_wait_teardown(bar(Lay::B_DRAIN), 0);
     }
-   }
   } else if (warp < 12) {
     // ---------------------------------------------------------------- compute: P^T and dS^T
     set_regs_inc<kRegsCompute>();

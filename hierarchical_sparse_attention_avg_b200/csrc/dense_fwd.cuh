@@ -3,18 +3,19 @@
 //   O = softmax(Z + mask) V,  Z = cap tanh(scale Q K^T / cap) + bias(h, x - j),  LSE = log sum exp Z
 //
 // in one pass over the keys with a running maximum and sum per row.  One block per (batch, head group, pair of 128-row
-// query tiles, share of the keys), warp roles as in the gathered attention: warp 0 TMA producer, warp 1 MMA issuer,
-// warps 2-5 and 6-9 the softmax of "stream" 0 and 1, one query row (= TMEM lane) per thread.  A stream has its own
-// scores S (128 fp32 TMEM columns, the probabilities written over them as the A operand of the next product) and its
-// own accumulator O, so the tensor core works for one stream while the other's exponentials run.
+// query tiles, share of the keys) with two "streams".  A stream has its own scores S (128 fp32 TMEM columns, the
+// probabilities written over them as the A operand of the next product), its own accumulator O and four softmax warps, one
+// query row (= TMEM lane) per thread, so the tensor core works for one stream while the other's exponentials run.  Warps 0
+// and 3 are TMA producers, 1 and 2 MMA issuers, 4-7 and 8-11 the streams' softmax; the first four give registers to the
+// others (224 a thread: the 128 scores of a row and tile stay in registers).
 //
-// - Long queries: the two streams are two query tiles over the same keys.
+// - Long queries: the two streams are two query tiles over the same keys, from one producer, and one issuer alternates
+//   their products.
 // - At most one query tile per head group (single tokens, short chunks): both streams take the same queries, stream 0
 //   the even and stream 1 the odd key tiles of the block (`dual`), and are joined through shared memory at the end; the
 //   query heads of one key head share the 128 rows (`pack`), so the cache is read once for all of them; and where the
 //   blocks are fewer than the SMs, `nsplit` blocks share the keys, each writes its normalised fp32 rows and their LSE,
-//   and join_kernel adds them with weights exp(LSE - max LSE).
-//
+//   and join_kernel adds them with weights exp(LSE - max LSE).  Each stream has a producer, an issuer and a ring of its own.
 //   With at most 32 rows (`REP` = 4) the queries stand four times in the tile, once in each lane quarter, and a warp takes
 //   the 32 columns of its quarter: the exponentials of a key tile are spread over all four schedulers instead of one
 //   (each copy keeps its own maximum, sum and accumulator, with zeros for the other columns' probabilities).
@@ -22,7 +23,7 @@
 // The block first classes its key tiles for each stream (invisible / partly masked / distances of several buckets), one
 // byte each in shared memory, from the lengths and the ids' ranges of the tiles; every role walks the visible ones.
 // Scores are formed in the log2 domain.  A tile inside one bucket adds one constant per row; a tile across buckets
-// reads the bias from a window of distances in shared memory; slopes are one packed FMA on top.
+// reads the bias from a window of distances in shared memory; slopes are one FMA more.
 //
 // Masked places: a masked score is overwritten after it is computed, whatever it was.  A value row that is not finite
 // would still reach other rows through 0 * inf, so in tiles with masked pairs the softmax threads clear such rows of V
@@ -33,6 +34,7 @@
 // the running maximum itself, so that a row's largest one is 1 and exact: with a maximum that only moves when exceeded by
 // 2^8 the accumulator is rescaled more rarely (269 us instead of 275 at 16 heads of 8,192 causal keys), but <dO, O>, which
 // the backward subtracts from nearly equal numbers, then makes bf16 dQ and dK 2.8e-3 off instead of 2.4e-3.
+// fp16 probabilities are carried times 2^14, so that the many small ones of a long row beside one large key do not vanish.
 #pragma once
 
 #include <atomic>
@@ -69,8 +71,7 @@ struct FwdArgs {
   int pack, tok, rep, ntile, npair, nsplit, dual, head_fast, slots;
   uint32_t off_kv, off_bar, off_win, off_flags;
   int win;  // floats of one stream's bias window
-  DenseTensor v;
-  DenseTensor o, low;
+  DenseTensor v, o, low;
   float* lse;
   const int2* kdoc;
   float *part_o, *part_lse;
@@ -81,6 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     dense_fwd_kernel(const __grid_constant__ FwdMaps m, const __grid_constant__ FwdArgs p,
                      const __grid_constant__ BucketStarts starts) {
   constexpr uint32_t TILE = kTile * D * 2;
+  constexpr float kShift = F16 ? 14.f : 0.f;  // log2 of what the probabilities are carried times
   constexpr int ROWS = kTile / REP, CH = 4 / REP;  // rows of a copy of the queries; 32-column runs of a thread
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;  // columns: S/P of stream q at 128 q, O at 256 + 128 q
 
-  // Class every key tile for both streams.
+  // Class every key tile for both streams.  (Ids' ranges of few tiles are taken here: kOwnDocTiles.)
   const int nkt = (a.Skv + kTile - 1) / kTile;
   const bool own_docs = nkt <= kOwnDocTiles;
   if (a.docs) {
@@ -195,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Tiles are taken from the last to the first: a causal row's own neighbourhood, where slopes and learned biases are
   // largest, comes first, and the maximum seldom moves afterwards.
   const int first = s_first, last = s_last;  // first > last: none
-  const int all = p.dual ? 0 : 3;  // streams whose tiles a ring carries: both, or its own (1 << e)
   auto next = [&](int t, int mask) {  // the next tile below t that a stream of `mask` sees (< first: none)
     for (--t; t >= first && !(flags[t - ks] & mask); --t) {}
     return t;
@@ -209,153 +210,153 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 4) {
-  set_regs_dec<kRegsIssue>();
-  if (warp == 0 || warp == 3) {
-    // ---------------------------------------------------------------- TMA producer of ring e
-    const int e = warp == 0 ? 0 : 1, mask = all ? all : 1 << e;
-    if (lane == 0 && first <= last && (e == 0 || p.dual)) {
-      bool ok = true;
-      const int nqt = p.dual ? 1 : nstream;
-      if (e == 0) {
-        mbar_arrive_expect_tx(bar(kBQ), nqt * REP * p.pack * p.tok * D * 2);
-        for (int q = 0; q < nqt; ++q)
-          for (int db = 0; db < D / 64; ++db)
-            for (int c = 0; c < REP; ++c)
-              tma_load_5d(sb + q * TILE + db * 16384 + c * ROWS * 128, &m.q, bar(kBQ), db * 64, 0, tok0(q), hp, b);
+    set_regs_dec<kRegsIssue>();
+    if (warp == 0 || warp == 3) {
+      // ---------------------------------------------------------------- TMA producer of ring e
+      const int e = warp == 0 ? 0 : 1, mask = p.dual ? 1 << e : 3;  // of the streams it feeds
+      if (lane == 0 && first <= last && (e == 0 || p.dual)) {
+        bool ok = true;
+        const int nqt = p.dual ? 1 : nstream;
+        if (e == 0) {
+          mbar_arrive_expect_tx(bar(kBQ), nqt * REP * p.pack * p.tok * D * 2);
+          for (int q = 0; q < nqt; ++q)
+            for (int db = 0; db < D / 64; ++db)
+              for (int c = 0; c < REP; ++c)
+                tma_load_5d(sb + q * TILE + db * 16384 + c * ROWS * 128, &m.q, bar(kBQ), db * 64, 0, tok0(q), hp, b);
+        }
+        int n = 0;  // loads
+        Ring r;
+        for (int t = next(last + 1, mask); t >= first && ok; t = next(t, mask))
+          for (int kv = 0; kv < 2; ++kv) {
+            const int slot = e * p.slots + r.s;
+            if (n >= p.slots) ok = mbar_wait(bar(kBFree + slot), r.ph ^ 1, &s_wait, status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(bar(kBFull + slot), TILE);
+            for (int db = 0; db < D / 64; ++db)
+              tma_load_5d(sb + p.off_kv + slot * TILE + db * 16384, kv ? &m.v : &m.k, bar(kBFull + slot), db * 64, 0,
+                          t * kTile, kvh, b);
+            ++n;
+            r.step(p.slots);
+          }
+        // every copy has landed before the block lets go of its memory, whoever gave up
+        if (e == 0) mbar_wait_teardown(bar(kBQ), 0);
+        for (int i = n > p.slots ? n - p.slots : 0; i < n; ++i)
+          mbar_wait_teardown(bar(kBFull + e * p.slots + i % p.slots), (i / p.slots) & 1);
       }
-      int n = 0;  // loads
-      Ring r;
-      for (int t = next(last + 1, mask); t >= first && ok; t = next(t, mask))
-        for (int kv = 0; kv < 2; ++kv) {
-          const int slot = e * p.slots + r.s;
-          if (n >= p.slots) ok = mbar_wait(bar(kBFree + slot), r.ph ^ 1, &s_wait, status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(bar(kBFull + slot), TILE);
-          for (int db = 0; db < D / 64; ++db)
-            tma_load_5d(sb + p.off_kv + slot * TILE + db * 16384, kv ? &m.v : &m.k, bar(kBFull + slot), db * 64, 0,
-                        t * kTile, kvh, b);
-          ++n;
-          r.step(p.slots);
-        }
-      // every copy has landed before the block lets go of its memory, whoever gave up
-      if (e == 0) mbar_wait_teardown(bar(kBQ), 0);
-      for (int i = n > p.slots ? n - p.slots : 0; i < n; ++i)
-        mbar_wait_teardown(bar(kBFull + e * p.slots + i % p.slots), (i / p.slots) & 1);
-    }
-  } else {
-    // ---------------------------------------------------------------- MMA issuers (whole warps, one lane issuing)
-    const int me = warp == 1 ? 0 : 1;
-    if (first <= last && (me == 0 || p.dual)) {
-      constexpr int fmt = F16 ? kFmtF16 : kFmtBF16;
-      constexpr uint32_t idesc_qk = idesc_f32acc(fmt, 128, 128, 0, 0);
-      constexpr uint32_t idesc_pv = idesc_f32acc(fmt, 128, D, 0, 1);
-      const uint32_t leader = elect_one();
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t dQ = sdesc_sw128(sb, 16, 1024);
-      const uint64_t dK = sdesc_sw128(sb + p.off_kv, 16, 1024), dV = sdesc_sw128(sb + p.off_kv, 16384, 1024);
-      auto wait = [&](int i, uint32_t ph) {
-        return __all_sync(0xffffffffu, mbar_wait(bar(i), ph, &s_wait, status)) != 0;
-      };
-      auto scores = [&](int q, int slot) {  // S_q = Q_q K^T
-        const uint64_t q0 = dQ + (p.dual ? 0 : q) * (TILE >> 4), k0 = dK + slot * (TILE >> 4);
+    } else {
+      // ---------------------------------------------------------------- MMA issuers (whole warps, one lane issuing)
+      const int me = warp == 1 ? 0 : 1;
+      if (first <= last && (me == 0 || p.dual)) {
+        constexpr int fmt = F16 ? kFmtF16 : kFmtBF16;
+        constexpr uint32_t idesc_qk = idesc_f32acc(fmt, 128, 128, 0, 0);
+        constexpr uint32_t idesc_pv = idesc_f32acc(fmt, 128, D, 0, 1);
+        const uint32_t leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dQ = sdesc_sw128(sb, 16, 1024);
+        const uint64_t dK = sdesc_sw128(sb + p.off_kv, 16, 1024), dV = sdesc_sw128(sb + p.off_kv, 16384, 1024);
+        auto wait = [&](int i, uint32_t ph) {
+          return __all_sync(0xffffffffu, mbar_wait(bar(i), ph, &s_wait, status)) != 0;
+        };
+        auto scores = [&](int q, int slot) {  // S_q = Q_q K^T
+          const uint64_t q0 = dQ + (p.dual ? 0 : q) * (TILE >> 4), k0 = dK + slot * (TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          umma_ss_by(leader, tm + 128 * q, q0 + ko, k0 + ko, idesc_qk, kk > 0 ? 1u : 0u);
-        }
-        umma_commit_by(leader, bar(kBSF + q));
-      };
-      // O_q (+)= P_q V, the keys of each half of the tile as soon as their probabilities are there
-      auto values = [&](int q, int slot, bool add, uint32_t ph) {
-        const uint64_t v0 = dV + slot * (TILE >> 4);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            umma_ss_by(leader, tm + 128 * q, q0 + ko, k0 + ko, idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          umma_commit_by(leader, bar(kBSF + q));
+        };
+        // O_q (+)= P_q V, the keys of each half of the tile as soon as their probabilities are there
+        auto values = [&](int q, int slot, bool add, uint32_t ph) {
+          const uint64_t v0 = dV + slot * (TILE >> 4);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          if (!wait(kBPF + 2 * hh + q, ph)) return false;
-          tc_fence_after();
+          for (int hh = 0; hh < 2; ++hh) {
+            if (!wait(kBPF + 2 * hh + q, ph)) return false;
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 4 * hh; kk < 4 * hh + 4; ++kk)
-            umma_ts_by(leader, tm + 256 + 128 * q, tm + 128 * q + kk * 8, v0 + kk * (2048 >> 4), idesc_pv,
-                       (add || kk > 0) ? 1u : 0u);
-        }
-        return true;
-      };
-      // A stream's next scores are issued right behind its product: they overwrite P once the product has read it, and
-      // their commit tells the softmax that the product is done.
-      bool ok = wait(kBQ, 0);
-      Ring r;
-      if (p.dual) {  // an issuer per stream: one alone would be busy for longer than the tensor core
-        const int mask = 1 << me, s0 = me * p.slots;
-        int t = next(last + 1, mask);
-        if (ok && t >= first) {
-          ok = wait(kBFull + s0, 0);
+            for (int kk = 4 * hh; kk < 4 * hh + 4; ++kk)
+              umma_ts_by(leader, tm + 256 + 128 * q, tm + 128 * q + kk * 8, v0 + kk * (2048 >> 4), idesc_pv,
+                         (add || kk > 0) ? 1u : 0u);
+          }
+          return true;
+        };
+        // A stream's next scores are issued right behind its product: they overwrite P once the product has read it, and
+        // their commit tells the softmax that the product is done.
+        bool ok = wait(kBQ, 0);
+        Ring r;
+        if (p.dual) {  // an issuer per stream: one alone would be busy for longer than the tensor core
+          const int mask = 1 << me, s0 = me * p.slots;
+          int t = next(last + 1, mask);
+          if (ok && t >= first) {
+            ok = wait(kBFull + s0, 0);
+            if (ok) {
+              tc_fence_after();
+              scores(me, s0);
+              umma_commit_by(leader, bar(kBFree + s0));
+              r.step(p.slots);
+            }
+          }
+          for (int n = 0; t >= first && ok; ++n) {
+            // while the softmax works: the tile's values, and the next tile's keys
+            const int sv = s0 + r.s, tn = next(t, mask);
+            ok = wait(kBFull + sv, r.ph);
+            r.step(p.slots);
+            const int sk = s0 + r.s;
+            if (ok && tn >= first) ok = wait(kBFull + sk, r.ph);
+            if (ok) ok = values(me, sv, n > 0, n & 1);
+            if (!ok) break;
+            if (tn >= first) {
+              scores(me, sk);
+              umma_commit_by(leader, bar(kBFree + sv));
+              umma_commit_by(leader, bar(kBFree + sk));
+              r.step(p.slots);
+            }
+            t = tn;
+          }
+          umma_commit_by(leader, bar(kBOD + me));
+        } else {
+          // both streams see the same tiles: one issuer alternates them, O_0 += P_0 V | S_0 next | O_1 += P_1 V | S_1 next,
+          // so that one stream's products run under the other's softmax
+          ok = ok && wait(kBFull, 0);
+          int t = last;
           if (ok) {
             tc_fence_after();
-            scores(me, s0);
-            umma_commit_by(leader, bar(kBFree + s0));
+            const int f = flags[t - ks];
+            if (f & 1) scores(0, 0);
+            if (f & 2) scores(1, 0);
+            umma_commit_by(leader, bar(kBFree));
             r.step(p.slots);
           }
-        }
-        for (int n = 0; t >= first && ok; ++n) {
-          // while the softmax works: the tile's values, and the next tile's keys
-          const int sv = s0 + r.s, tn = next(t, mask);
-          ok = wait(kBFull + sv, r.ph);
-          r.step(p.slots);
-          const int sk = s0 + r.s;
-          if (ok && tn >= first) ok = wait(kBFull + sk, r.ph);
-          if (ok) ok = values(me, sv, n > 0, n & 1);
-          if (!ok) break;
-          if (tn >= first) {
-            scores(me, sk);
-            umma_commit_by(leader, bar(kBFree + sv));
-            umma_commit_by(leader, bar(kBFree + sk));
+          int cnt[2] = {0, 0};
+          while (t >= first && ok) {
+            const int ta = next(t, 3), f = flags[t - ks], fa = ta >= first ? flags[ta - ks] : 0;
+            const int sv = r.s;
+            ok = wait(kBFull + sv, r.ph);
             r.step(p.slots);
-          }
-          t = tn;
-        }
-        umma_commit_by(leader, bar(kBOD + me));
-      } else {
-        // both streams see the same tiles: one issuer alternates them, O_0 += P_0 V | S_0 next | O_1 += P_1 V | S_1 next,
-        // so that one stream's products run under the other's softmax
-        ok = ok && wait(kBFull, 0);
-        int t = last;
-        if (ok) {
-          tc_fence_after();
-          const int f = flags[t - ks];
-          if (f & 1) scores(0, 0);
-          if (f & 2) scores(1, 0);
-          umma_commit_by(leader, bar(kBFree));
-          r.step(p.slots);
-        }
-        int cnt[2] = {0, 0};
-        while (t >= first && ok) {
-          const int ta = next(t, 3), f = flags[t - ks], fa = ta >= first ? flags[ta - ks] : 0;
-          const int sv = r.s;
-          ok = wait(kBFull + sv, r.ph);
-          r.step(p.slots);
-          if (ok && fa) ok = wait(kBFull + r.s, r.ph);  // the next keys too, while the softmax works
+            if (ok && fa) ok = wait(kBFull + r.s, r.ph);  // the next keys too, while the softmax works
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            if (ok && (f >> q & 1)) {
-              ok = values(q, sv, cnt[q] > 0, cnt[q] & 1);
-              ++cnt[q];
+            for (int q = 0; q < 2; ++q) {
+              if (ok && (f >> q & 1)) {
+                ok = values(q, sv, cnt[q] > 0, cnt[q] & 1);
+                ++cnt[q];
+              }
+              if (ok && (fa >> q & 1)) scores(q, r.s);
             }
-            if (ok && (fa >> q & 1)) scores(q, r.s);
+            if (!ok) break;
+            umma_commit_by(leader, bar(kBFree + sv));
+            if (ta >= first) {
+              umma_commit_by(leader, bar(kBFree + r.s));
+              r.step(p.slots);
+            }
+            t = ta;
           }
-          if (!ok) break;
-          umma_commit_by(leader, bar(kBFree + sv));
-          if (ta >= first) {
-            umma_commit_by(leader, bar(kBFree + r.s));
-            r.step(p.slots);
-          }
-          t = ta;
+          umma_commit_by(leader, bar(kBOD + 0));
+          umma_commit_by(leader, bar(kBOD + 1));
         }
-        umma_commit_by(leader, bar(kBOD + 0));
-        umma_commit_by(leader, bar(kBOD + 1));
+        umma_commit_by(leader, bar(kBDrain + me));  // every product issued above completes before the block lets go
+        mbar_wait_teardown(bar(kBDrain + me), 0);
       }
-      umma_commit_by(leader, bar(kBDrain + me));  // every product issued above completes before the block lets go
-      mbar_wait_teardown(bar(kBDrain + me), 0);
     }
-  }
   } else {
     set_regs_inc<kRegsSoftmax>();
     // ---------------------------------------------------------------- softmax (warps 4..7: stream 0, 8..11: stream 1)
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           // P over the first 64 columns of S, and its row sum; a row that has seen no key yet keeps P = 0
-          const float sub = cadd - (m_run == -INFINITY ? 0.f : m_run);
+          const float sub = cadd + kShift - (m_run == -INFINITY ? 0.f : m_run);
           uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
           const uint64_t mul2 = f2pack(mul, mul), sub2 = f2pack(sub, sub), one2 = f2pack(1.f, 1.f);
           auto pair = [&](int c, int i) {  // the probabilities of columns i, i + 1 of run c, packed
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto stats = [&](int64_t ri, float m, float l) {
-        const float l2 = l == 0.f ? -INFINITY : m + __log2f(l);
+        const float l2 = l == 0.f ? -INFINITY : m - kShift + __log2f(l);
         if (part) p.part_lse[pbase + ri] = l2;
         else p.lse[ri] = l2 * kLn2;
       };

@@ -110,6 +110,22 @@ def test_default_outputs_follow_their_inputs(lh, cuda_device):
         A.check(n, t, ref)
 
 
+@pytest.mark.parametrize("Sq", [1, 200])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_many_small_probabilities_beside_a_large_one(lh, cuda_device, dtype, Sq):
+    """One key 18 (natural) above 20,000 others: what they have in common must not round away."""
+    S = 20200
+    P = lh.AttnParams(1, 2, 1, Sq, S, 64, dtype=dtype, causal=False, scale=1.0)
+    q, k, v = (torch.zeros(1, h, n, 64, dtype=dtype, device=cuda_device) for h, n in ((2, Sq), (1, S), (1, S)))
+    q[..., 0], k[:, :, 7, 0] = 1.0, 18.0
+    v[:] = 1.0
+    v[:, :, 7] = 0.0
+    ref = A.reference(P, q, k, v)
+    o, lse = lh.lh_attn_forward(P, q, k, v)
+    A.check("o", o, ref, tiny=0.0)  # 3e-4 everywhere
+    A.check("lse", lse, ref)
+
+
 def test_many_documents_beyond_the_own_ranges(lh, cuda_device):
     S = 4500  # more key tiles than a block classes by itself
     P = lh.AttnParams(1, 2, 1, S, S, 64, softcap=50.0)
