@@ -95,12 +95,18 @@ DenseFwdPlan dense_fwd_plan(const DenseDims& a) {
   const int npair = f.dual ? 1 : (f.ntile + 1) / 2;
   const int64_t blocks = (int64_t)a.B * (a.Hq / f.pack) * npair;
   const int nk = (a.Skv + kTile - 1) / kTile;
-  // Too few blocks for the SMs: as many shares of the keys as fill them once, of four tiles at least.
+  // Fewer blocks than SMs: the shares of the keys that are through first, counted in key tiles: rounds of blocks times a
+  // block's tiles and about four for its start and end, and two for the join (120 blocks in one round against 280 in two,
+  // 9 x 128-row tiles over 128 key tiles: 134 us against 127).
   f.nsplit = 1;
-  if (blocks <= kSms / 2) {
-    f.nsplit = (int)(kSms / blocks);
-    if (f.nsplit > (nk + 3) / 4) f.nsplit = (nk + 3) / 4;
-    if (f.nsplit < 1) f.nsplit = 1;
+  int64_t best = nk + 4;
+  for (int rounds = 1; blocks < kSms && rounds <= 2; ++rounds) {
+    const int n = (int)(rounds * kSms / blocks) < nk / 4 ? (int)(rounds * kSms / blocks) : nk / 4;
+    const int64_t cost = n > 1 ? (blocks * n + kSms - 1) / kSms * ((nk + n - 1) / n + 4) + 2 : INT64_MAX;
+    if (cost < best) {
+      best = cost;
+      f.nsplit = n;
+    }
   }
   return f;
 }
