@@ -415,13 +415,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             run_b = bucket;
             run += f2lo(sum2) + f2hi(sum2);
           } else {
-            // diagonals: after step c lane r holds, of distance base + ((c - r) mod 32), `up`, and of 32 less, `dn`
-            float up = 0.f, dn = 0.f;
+            // diagonals: after step c lane r holds, of distance base + ((c - r) mod 32), `up`, and of 32 less, `dn`; four
+            // runs of eight columns side by side, each brought to the last one's place at the end
+            float ups[4] = {}, dns[4] = {};
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              up = __shfl_sync(0xffffffffu, up, (lane + 31) & 31);
-              dn = __shfl_sync(0xffffffffu, dn, (lane + 31) & 31);
-              if (lane <= c) up += dp[c]; else dn += dp[c];
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int c = 8 * k + e;
+                if (e > 0) {
+                  ups[k] = __shfl_sync(0xffffffffu, ups[k], (lane + 31) & 31);
+                  dns[k] = __shfl_sync(0xffffffffu, dns[k], (lane + 31) & 31);
+                }
+                if (lane <= c) ups[k] += dp[c]; else dns[k] += dp[c];
+              }
+            float up = ups[3], dn = dns[3];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              up += __shfl_sync(0xffffffffu, ups[k], (lane + 8 * k + 8) & 31);
+              dn += __shfl_sync(0xffffffffu, dns[k], (lane + 8 * k + 8) & 31);
             }
             // lane r: up is distance base + 31 - r, dn base - 1 - r; sums over the lanes from r on are prefixes
 #pragma unroll
