@@ -110,6 +110,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nk = (len + kTile - 1) / kTile, per = (nk + p.nsplit - 1) / p.nsplit;
   const int ks = split * per, ke = min(nk, ks + per);  // key tiles of this block
 
+  auto load = [&](const CUtensorMap* map, int slot, int t) {  // a key or value tile
+    mbar_arrive_expect_tx(bar(kBFull + slot), TILE);
+    for (int db = 0; db < D / 64; ++db)
+      tma_load_5d(sb + p.off_kv + slot * TILE + db * 16384, map, bar(kBFull + slot), db * 64, 0, t * kTile, kvh, b);
+  };
+  auto load_q = [&]() {
+    const int nqt = p.dual ? 1 : nstream;
+    mbar_arrive_expect_tx(bar(kBQ), nqt * REP * p.pack * p.tok * D * 2);
+    for (int q = 0; q < nqt; ++q)
+      for (int db = 0; db < D / 64; ++db)
+        for (int c = 0; c < REP; ++c)
+          tma_load_5d(sb + q * TILE + db * 16384 + c * ROWS * 128, &m.q, bar(kBQ), db * 64, 0, tok0(q), hp, b);
+  };
+
   if (threadIdx.x == 0) {
     wait_ctl_init(&s_wait, status);
     mbar_init(bar(kBQ), 1);
@@ -129,12 +143,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kBDrain), 1);
     mbar_init(bar(kBDrain + 1), 1);
     fence_mbar_init();
+    fence_proxy_async_smem();  // (the first copies may be this thread's)
     s_first = INT32_MAX;
     s_last = -1;
     s_bad = 0;
-    prefetch_tmap(&m.q);
-    prefetch_tmap(&m.k);
-    prefetch_tmap(&m.v);
+    if (!a.docs) {  // the last visible tile is known without its flags: its copies go out before anything else
+      const int lk = last_key(a, off + min(tok0(nstream - 1) + p.tok, a.Sq) - 1, len, prefix);
+      const int t = lk < 0 ? -1 : min(lk / kTile, ke - 1);
+      if (t >= ks) {
+        load_q();
+        const int e = p.dual ? (t - ks) & 1 : 0;
+        load(&m.k, e * p.slots, t);
+        load(&m.v, e * p.slots + 1, t);
+      }
+    } else {
+      prefetch_tmap(&m.q);
+      prefetch_tmap(&m.k);
+      prefetch_tmap(&m.v);
+    }
   }
   if (warp == 1) tmem_alloc(smem_u32(&s_tmem), 512);
   if (BIAS == 2)
@@ -216,14 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e = warp == 0 ? 0 : 1, mask = p.dual ? 1 << e : 3;  // of the streams it feeds
       if (lane == 0 && first <= last && (e == 0 || p.dual)) {
         bool ok = true;
-        const int nqt = p.dual ? 1 : nstream;
-        if (e == 0) {
-          mbar_arrive_expect_tx(bar(kBQ), nqt * REP * p.pack * p.tok * D * 2);
-          for (int q = 0; q < nqt; ++q)
-            for (int db = 0; db < D / 64; ++db)
-              for (int c = 0; c < REP; ++c)
-                tma_load_5d(sb + q * TILE + db * 16384 + c * ROWS * 128, &m.q, bar(kBQ), db * 64, 0, tok0(q), hp, b);
-        }
+        if (e == 0 && a.docs) load_q();
         int n = 0;  // loads
         Ring r;
         for (int t = next(last + 1, mask); t >= first && ok; t = next(t, mask))
@@ -231,10 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int slot = e * p.slots + r.s;
             if (n >= p.slots) ok = mbar_wait(bar(kBFree + slot), r.ph ^ 1, &s_wait, status);
             if (!ok) break;
-            mbar_arrive_expect_tx(bar(kBFull + slot), TILE);
-            for (int db = 0; db < D / 64; ++db)
-              tma_load_5d(sb + p.off_kv + slot * TILE + db * 16384, kv ? &m.v : &m.k, bar(kBFull + slot), db * 64, 0,
-                          t * kTile, kvh, b);
+            if (a.docs || t != last) load(kv ? &m.v : &m.k, slot, t);  // (else it is on its way)
             ++n;
             r.step(p.slots);
           }
