@@ -610,7 +610,7 @@ def lh_attn_forward(P: AttnParams, q, k, v, slopes=None, table=None, docs=None, 
     if o is None:
         o = torch.empty_like(q)
     if lse is None:
-        lse = q.new_empty(qs[:3], dtype=torch.float32)
+        lse = torch.empty_strided(qs[:3], (P.Hq * P.Sq, P.Sq, 1), dtype=torch.float32, device=dev)
     dt = P.dtype
     rc = _on_device(dev, _lib.lh_attn_forward, P._ref, _attn_mods(P, dev, slopes, table, docs, prefix, kv_len),
                     _rows(q, qs, dt, dev, "q"), _rows(k, ks, dt, dev, "k"), _rows(v, ks, dt, dev, "v"),
