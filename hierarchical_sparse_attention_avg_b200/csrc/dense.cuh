@@ -59,7 +59,7 @@ __device__ __forceinline__ int dense_len(const DenseDims& a, int b) {
   return a.kv_len ? min(max(__ldg(a.kv_len + b), 0), a.Skv) : a.Skv;
 }
 __device__ __forceinline__ int dense_prefix(const DenseDims& a, int b, int len) {
-  return a.prefix ? min(__ldg(a.prefix + b), len) : 0;
+  return a.prefix ? min(max(__ldg(a.prefix + b), 0), len) : 0;
 }
 // Last key position that a row at x may see (-1: none); its own document apart.
 __device__ __forceinline__ int last_key(const DenseDims& a, int x, int len, int prefix) {

@@ -373,7 +373,7 @@ typedef struct lh_attn_mods {
   const float* slopes;    /* [Hq] */
   const void* table;      /* [Hq, buckets] (dtype); required iff buckets > 0 */
   const int32_t* docs;    /* [B, Skv] document of each position; NULL: one document */
-  const int32_t* prefix;  /* [B] (causal only) */
+  const int32_t* prefix;  /* [B] (causal only), clamped to [0, kv_len] */
   const int32_t* kv_len;  /* [B], clamped to [0, Skv]; NULL: Skv */
 } lh_attn_mods;
 

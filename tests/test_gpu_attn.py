@@ -78,6 +78,13 @@ FORWARD = {
     "group5_chunk": (dict(B=1, Hq=10, Hkv=2, Sq=60, Skv=2000, d=128, softcap=50.0), dict(kv_len=[1999])),
     "chunk": (dict(B=2, Hq=4, Hkv=2, Sq=257, Skv=4000, d=128, softcap=50.0), dict(kv_len=[4000, 300])),
     "long_cache": (dict(B=1, Hq=4, Hkv=2, Sq=1, Skv=70001, d=128), {}),
+    "bias_one": (dict(B=2, Hq=2, Hkv=1, Sq=1, Skv=1, d=64, buckets=32, max_distance=128), {}),
+    "group16_full": (dict(B=1, Hq=16, Hkv=1, Sq=8, Skv=700, d=128, buckets=32, max_distance=128, dtype=FP), {}),
+    "group16_two": (dict(B=1, Hq=16, Hkv=1, Sq=9, Skv=700, d=128, buckets=64, max_distance=500, softcap=20.0), {}),
+    "group16_copies": (dict(B=2, Hq=16, Hkv=1, Sq=2, Skv=900, d=128, buckets=32, max_distance=128), dict(kv_len=[900, 1])),
+    "group48": (dict(B=1, Hq=48, Hkv=1, Sq=1, Skv=300, d=64), dict(slopes=True)),
+    "few_rows_docs": (dict(B=2, Hq=4, Hkv=2, Sq=30, Skv=260, d=64, softcap=30.0),
+                      dict(docs=[spans(260, 100, 140), [3] * 60 + [1] * 200], kv_len=[250, 255])),
     "wide_grid": (dict(B=40, Hq=8, Hkv=4, Sq=1, Skv=400, d=64), dict(kv_len=[10 * i for i in range(40)])),
 }
 

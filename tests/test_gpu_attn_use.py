@@ -136,6 +136,58 @@ def test_many_documents_beyond_the_own_ranges(lh, cuda_device):
         A.check(n, t, ref)
 
 
+def test_extreme_ids_lengths_and_prefixes(lh, cuda_device):
+    """Ids at both ends of the type, lengths outside [0, Skv], prefixes below 0 and beyond the length."""
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    P = lh.AttnParams(4, 4, 2, 300, 300, 64)
+    ids = [[hi] * 100 + [0] * 80 + [lo] * 20 + [hi - 1] * 100, [lo] * 300, [hi] * 300, [0, hi] * 150]
+    m = mods(P, cuda_device, docs=ids, kv_len=[hi, 250, lo, 299], prefix=[lo, 10, hi, hi])
+    q, k, v, dout = A.make(P, 8, cuda_device, grad=True)
+    ref = A.reference(P, q, k, v, dout=dout, **m)
+    for n, g in _all(lh, P, q, k, v, dout, m).items():
+        A.check(n, g, ref)
+
+
+def test_largest_batch(lh, cuda_device):
+    P = lh.AttnParams(4095, 16, 16, 1, 5, 64)  # B Hq = 65,520
+    q, k, v, dout = A.make(P, 6, cuda_device, grad=True)
+    ref = A.reference(P, q, k, v, dout=dout)
+    for n, t in _all(lh, P, q, k, v, dout, {}).items():
+        A.check(n, t, ref)
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+def test_more_query_tiles_than_the_heads_first_grid_takes(lh, cuda_device, slopes):
+    """131,328 rows in documents of 128: the same as so many entries of 128 rows."""
+    n, w, d = 1026, 128, 64
+    P, E = lh.AttnParams(1, 1, 1, n * w, n * w, d), lh.AttnParams(n, 1, 1, w, w, d)
+    x = A.make(P, 9, cuda_device, grad=True)
+    m = mods(P, cuda_device, slopes=slopes)
+    docs = (torch.arange(n * w, device=cuda_device) // w).to(torch.int32)[None]
+    got = _all(lh, P, *x, dict(m, docs=docs))
+    short = [t.view(1, n, w, d).transpose(0, 1) for t in x]
+    ref = A.reference(E, *short[:3], dout=short[3], **m)
+    for name, t in got.items():
+        A.check(name, t.view(1, n, w, *t.shape[3:]).transpose(0, 1), ref)
+
+
+def test_offsets_beyond_32_bits(lh, cuda_device):
+    """A cache of 18 heads of 2^20 keys: 2.4e9 elements each of keys and values."""
+    H, S, d = 18, 1 << 20, 128
+    P = lh.AttnParams(1, H, H, 1, S, d)
+    g = torch.Generator(cuda_device).manual_seed(1)
+    k, v = (torch.randn(1, H, S, d, generator=g, device=cuda_device, dtype=BF) for _ in range(2))
+    q = torch.randn(1, H, 1, d, generator=g, device=cuda_device, dtype=BF)
+    kv_len = torch.tensor([S - 3], dtype=torch.int32, device=cuda_device)
+    k[:, :, S - 3:], v[:, :, S - 3:] = math.nan, math.nan
+    o, lse = lh.lh_attn_forward(P, q, k, v, kv_len=kv_len)
+    one = lh.AttnParams(1, 1, 1, 1, S, d)
+    for h in (0, H - 1):
+        ref = A.reference(one, q[:, h:h + 1], k[:, h:h + 1], v[:, h:h + 1], kv_len=kv_len)
+        A.check("o", o[:, h:h + 1], ref)
+        A.check("lse", lse[:, h:h + 1], ref)
+
+
 def test_workspaces(lh, cuda_device):
     P = lh.AttnParams(1, 4, 2, 1, 3000, 128)
     q, k, v = A.make(P, 5, cuda_device)
