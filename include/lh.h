@@ -371,7 +371,8 @@ typedef struct lh_tensor {
 /* What shapes the scores besides the parameters; device pointers, each may be NULL. */
 typedef struct lh_attn_mods {
   const float* slopes;    /* [Hq] */
-  const void* table;      /* [Hq, buckets] (dtype); required iff buckets > 0 */
+  const void* table;      /* [Hq, buckets] (dtype); required iff buckets > 0.  An entry of -inf (or bf16's lowest value)
+                             hides its bucket's keys from the head's rows and has no gradient */
   const int32_t* docs;    /* [B, Skv] document of each position; NULL: one document */
   const int32_t* prefix;  /* [B] (causal only), clamped to [0, kv_len] */
   const int32_t* kv_len;  /* [B], clamped to [0, Skv]; NULL: Skv */
@@ -396,8 +397,8 @@ int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_ten
  * its query heads) and, with a table, dtable [Hq, buckets].  q, k, v, M as in the forward; o and lse its results.  low:
  * NULL, or the forward's: dZ = P (dP - <dout, o>) takes a small difference, so o's own rounding is the largest error of
  * the gradients without it (bf16: dq, dk 2.4e-3 off the formula in the 2-norm with it, 4.2e-3 without, dtable up to
- * 7e-3).  dk, dv and dtable are bitwise reproducible; dq is accumulated with fp32 reduce-adds in no fixed order before
- * it is rounded. */
+ * 7e-3).  A bucket's dtable may also be off by 2^-20 of the |dZ| summed over the buckets next to it.  dk, dv and dtable
+ * are bitwise reproducible; dq is accumulated with fp32 reduce-adds in no fixed order before it is rounded. */
 int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
                      const lh_tensor* v, const lh_tensor* o, const lh_tensor* low, const float* lse,
                      const lh_tensor* dout, const lh_tensor* dq, const lh_tensor* dk, const lh_tensor* dv, void* dtable, void* ws,

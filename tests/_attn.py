@@ -72,7 +72,7 @@ def reference(P, q, k, v, slopes=None, table=None, docs=None, prefix=None, kv_le
     if table is not None:
         idx = bucket_index(far, P.buckets, P.max_distance, P.bidirectional)
         z = z + table.to(F8)[:, idx].transpose(0, 1)
-    mm = m[:, None].expand_as(z)
+    mm = m[:, None].expand_as(z) & (z > -1e38)  # a table's -inf or lowest value masks its bucket
     zmax = torch.where(mm, z.abs(), torch.zeros_like(z)).amax(3)
     z = z.masked_fill(~mm, -math.inf)
     lse = torch.logsumexp(z, 3)

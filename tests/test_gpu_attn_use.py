@@ -54,6 +54,26 @@ def test_dead_positions_hold_anything(lh, cuda_device, name, p, m, junk):
     assert lh.lh_get_status() == lh.LH_OK
 
 
+@pytest.mark.parametrize("ban", [-math.inf, torch.finfo(BF).min])
+@pytest.mark.parametrize("name,p,m,which", [
+    ("self", dict(B=2, Hq=4, Hkv=2, Sq=300, Skv=300, d=64), dict(docs=[spans(300, 100, 7, 193), spans(300, 300)]), [0]),
+    ("far", dict(B=1, Hq=2, Hkv=1, Sq=700, Skv=700, d=128, softcap=20.0), {}, [31, 20]),
+    ("all", dict(B=1, Hq=2, Hkv=2, Sq=150, Skv=150, d=64), {}, list(range(32))),
+    ("both", dict(B=2, Hq=4, Hkv=4, Sq=200, Skv=200, d=64, causal=False, bidirectional=True),
+     dict(docs=[spans(200, 150), spans(200, 200)]), [0, 15, 20]),
+    ("token", dict(B=3, Hq=8, Hkv=2, Sq=1, Skv=900, d=128), dict(kv_len=[900, 131, 1]), [31, 0]),
+    ("split", dict(B=1, Hq=4, Hkv=2, Sq=5, Skv=6000, d=64), {}, [31]),
+])
+def test_table_entries_that_mask_their_bucket(lh, cuda_device, name, p, m, which, ban):
+    P = lh.AttnParams(**p, buckets=32, max_distance=128)
+    q, k, v, dout = A.make(P, 3, cuda_device, grad=True)
+    m = mods(P, cuda_device, **m)
+    m["table"][:, which] = ban
+    ref = A.reference(P, q, k, v, dout=dout, **m)
+    for n, g in _all(lh, P, q, k, v, dout, m).items():
+        A.check(n, g, ref)
+
+
 @pytest.mark.parametrize("junk", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("p", [dict(d=128), dict(d=64, softcap=20.0), dict(d=64, dtype=FP, buckets=32, max_distance=128)])
 def test_masked_values_reach_no_row(lh, cuda_device, p, junk):
