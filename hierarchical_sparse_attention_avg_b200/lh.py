@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -502,10 +502,7 @@ class AttnParams:
     def __post_init__(self):
         if self.dtype not in _ATTN_DTYPES:
             raise ValueError(f"dtype: expected torch.bfloat16 or torch.float16, got {self.dtype}")
-        scale = (self.d ** -0.5 if self.d > 0 else 1.0) if self.scale is None else self.scale
-        c = LhAttnParams(self.B, self.Hq, self.Hkv, self.Sq, self.Skv, self.d, _ATTN_DTYPES[self.dtype],
-                         1 if self.causal else 0, scale, self.softcap, self.buckets, self.max_distance,
-                         1 if self.bidirectional else 0)
+        c = self.c()
         object.__setattr__(self, "_c", c)  # read by every call, built once
         object.__setattr__(self, "_ref", ctypes.addressof(c))
         object.__setattr__(self, "_status", _lib.lh_attn_validate(self._ref))
@@ -513,7 +510,14 @@ class AttnParams:
         object.__setattr__(self, "_ks", (self.B, self.Hkv, self.Skv, self.d))
 
     def c(self) -> LhAttnParams:
-        return self._c
+        scale = (self.d ** -0.5 if self.d > 0 else 1.0) if self.scale is None else self.scale
+        return LhAttnParams(self.B, self.Hq, self.Hkv, self.Sq, self.Skv, self.d, _ATTN_DTYPES[self.dtype],
+                            1 if self.causal else 0, scale, self.softcap, self.buckets, self.max_distance,
+                            1 if self.bidirectional else 0)
+
+    def __reduce__(self):
+        """Copies and pickles are made anew from the fields: ``_ref`` is the address of this object's own struct."""
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
 
 
 def lh_attn_validate(P: AttnParams) -> int:

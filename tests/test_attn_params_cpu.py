@@ -1,0 +1,42 @@
+"""``AttnParams`` as an ordinary value: copied, pickled, replaced and out of range."""
+
+from __future__ import annotations
+
+import copy
+import ctypes
+import dataclasses
+import gc
+import pickle
+
+import pytest
+import torch
+
+from hierarchical_sparse_attention_avg_b200 import lh
+
+OK = dict(B=2, Hq=4, Hkv=2, Sq=16, Skv=64, d=64)
+TABLE = dict(OK, dtype=torch.float16, causal=False, scale=0.3, softcap=20.0, buckets=32, max_distance=128, bidirectional=True)
+
+
+@pytest.mark.parametrize("fields", [OK, TABLE])
+@pytest.mark.parametrize("again", [copy.copy, copy.deepcopy, lambda p: pickle.loads(pickle.dumps(p)), dataclasses.replace,
+                                   lambda p: copy.deepcopy({"attn": [p]})["attn"][0]],
+                         ids=["copy", "deepcopy", "pickle", "replace", "nested"])
+def test_copies_hold_their_own_sizes(fields, again):
+    P = lh.AttnParams(**fields)
+    want = (lh.lh_attn_validate(P), lh.lh_attn_workspace_bytes(P), lh.lh_attn_workspace_bytes(P, True))
+    Q = again(P)
+    assert Q == P and hash(Q) == hash(P) and Q is not P
+    # the address that the calls pass is that of the copy's own struct (checked before anything reads through it)
+    assert Q._ref == ctypes.addressof(Q._c) and (Q._c is not P._c)
+    assert bytes(Q._c) == bytes(P._c)
+    del P
+    gc.collect()
+    others = [lh.AttnParams(B=1, Hq=1, Hkv=1, Sq=1, Skv=1, d=96) for _ in range(64)]  # what the freed memory may hold now
+    assert (lh.lh_attn_validate(Q), lh.lh_attn_workspace_bytes(Q), lh.lh_attn_workspace_bytes(Q, True)) == want
+    assert len(others) == 64
+
+
+def test_the_struct_that_calls_read_is_not_handed_out():
+    P = lh.AttnParams(**OK)
+    P.c().d = 128
+    assert P.c().d == P._c.d == 64
