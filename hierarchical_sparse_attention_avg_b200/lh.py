@@ -502,6 +502,9 @@ class AttnParams:
     def __post_init__(self):
         if self.dtype not in _ATTN_DTYPES:
             raise ValueError(f"dtype: expected torch.bfloat16 or torch.float16, got {self.dtype}")
+        for n in ("B", "Hq", "Hkv", "Sq", "Skv", "d", "buckets", "max_distance"):
+            if not -2 ** 31 <= getattr(self, n) < 2 ** 31:  # (ctypes would drop the upper bits)
+                raise ValueError(f"{n}: expected a 32-bit number, got {getattr(self, n)}")
         c = self.c()
         object.__setattr__(self, "_c", c)  # read by every call, built once
         object.__setattr__(self, "_ref", ctypes.addressof(c))

@@ -40,3 +40,12 @@ def test_the_struct_that_calls_read_is_not_handed_out():
     P = lh.AttnParams(**OK)
     P.c().d = 128
     assert P.c().d == P._c.d == 64
+
+
+@pytest.mark.parametrize("change", [dict(max_distance=2 ** 32 + 128), dict(B=2 ** 32 + 1), dict(Sq=2 ** 31), dict(Skv=-2 ** 32 + 64),
+                                    dict(buckets=2 ** 32), dict(Hq=2 ** 32 + 4), dict(d=2 ** 32 + 64)])
+def test_sizes_beyond_32_bits_are_refused(change):
+    """The library's sizes are 32-bit: a larger one is not cut down to another one."""
+    with pytest.raises(ValueError):
+        lh.AttnParams(**{**TABLE, **change})
+    assert lh.lh_attn_validate(lh.AttnParams(**dict(TABLE, max_distance=2 ** 31 - 1))) == lh.LH_OK
