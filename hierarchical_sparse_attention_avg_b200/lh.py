@@ -634,6 +634,8 @@ def lh_attn_backward(P: AttnParams, q, k, v, o, lse, dout, slopes=None, table=No
     ``low`` are its results, the other arguments those it got.  ``ws``: from ``new_attn_workspace(..., backward=True)``."""
     if P._status:
         _check(P._status, "lh_attn_backward")
+    if P.buckets and table is None:
+        _check(LH_ERR_INVALID_ARG, "lh_attn_backward")
     dev = q.device
     ws = _attn_ws(P, ws, dev, True, "lh_attn_backward")
     qs, ks = P._qs, P._ks

@@ -49,3 +49,13 @@ def test_sizes_beyond_32_bits_are_refused(change):
     with pytest.raises(ValueError):
         lh.AttnParams(**{**TABLE, **change})
     assert lh.lh_attn_validate(lh.AttnParams(**dict(TABLE, max_distance=2 ** 31 - 1))) == lh.LH_OK
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_backward_without_its_table_is_refused(given):
+    P = lh.AttnParams(**TABLE)
+    q, k = (torch.zeros(P.B, h, s, P.d, dtype=P.dtype) for h, s in ((P.Hq, P.Sq), (P.Hkv, P.Skv)))
+    dtable = torch.zeros(P.Hq, P.buckets, dtype=P.dtype) if given else None
+    with pytest.raises(lh.LighthouseError) as e:
+        lh.lh_attn_backward(P, q, k, k, q, torch.zeros(P.B, P.Hq, P.Sq), q, dtable=dtable)
+    assert e.value.status == lh.LH_ERR_INVALID_ARG
