@@ -56,8 +56,9 @@ void dense_sizes(const lh_attn_params& P, DenseDims* a, BucketStarts* bs) {
   a->buckets = P.buckets;
   bucket_starts(P, bs);
   if (P.buckets) {  // beyond the last bucket's first size, and beyond the longest distance, nothing changes
+    const int64_t longest = (int64_t)P.Skv + P.Sq;
     a->near = bs->start[bs->n - 1];
-    if (a->near > P.Skv + P.Sq) a->near = P.Skv + P.Sq;
+    if (a->near > longest) a->near = (int)longest;
   }
 }
 

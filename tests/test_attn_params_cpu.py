@@ -59,3 +59,15 @@ def test_backward_without_its_table_is_refused(given):
     with pytest.raises(lh.LighthouseError) as e:
         lh.lh_attn_backward(P, q, k, k, q, torch.zeros(P.B, P.Hq, P.Sq), q, dtable=dtable)
     assert e.value.status == lh.LH_ERR_INVALID_ARG
+
+
+def test_workspace_of_the_longest_queries():
+    """Rows near 2^31 over 2^20 keys: the span of distances, their sum, stays positive."""
+    size = lambda Sq: lh.lh_attn_workspace_bytes(lh.AttnParams(B=1, Hq=1, Hkv=1, Sq=Sq, Skv=1 << 20, d=64, buckets=32,  # noqa: E731
+                                                               max_distance=2 ** 31 - 1), True)
+    sizes = [size(Sq) for Sq in (2 ** 30, 2 ** 31 - 2 ** 21, 2 ** 31 - 2 ** 19, 2 ** 31 - 1)]
+    assert sizes == sorted(sizes)
+    # at least the fp32 accumulator of dq and the bias of each distance up to the last bucket's first one
+    near = min(lh.lh_attn_bucket_starts(lh.AttnParams(B=1, Hq=1, Hkv=1, Sq=1, Skv=1, d=64, buckets=32, max_distance=2 ** 31 - 1))[-1],
+               2 ** 31 - 1 + 2 ** 20)
+    assert sizes[-1] >= (2 ** 31 - 1) * 64 * 4 + 2 * near * 5
