@@ -113,8 +113,8 @@ DenseWs dense_ws(const DenseDims& a) {
   w.part_lse = take(rows * 4);
   w.fwd_total = o;
   o = w.part_o;
-  w.qdoc = take((size_t)a.B * ((a.Sq + 63) / 64) * sizeof(int2));
-  w.stats = take(2 * bhq * ((a.Sq + 3) & ~3) * 4);
+  w.qdoc = take(a.B * (((size_t)a.Sq + 63) / 64) * sizeof(int2));
+  w.stats = take(2 * bhq * (((size_t)a.Sq + 3) & ~(size_t)3) * 4);
   w.amax = take(bhk * 8);
   w.dqacc = take(bhq * a.Sq * a.d * 4);
   const int shares = dense_bwd_shares(a);

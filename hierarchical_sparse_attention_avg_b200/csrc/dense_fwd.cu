@@ -79,10 +79,10 @@ DenseFwdPlan dense_fwd_plan(const DenseDims& a) {
   // The query heads of a key head share query tiles where that takes fewer of them than tiles of one head each (few
   // tokens; at most 16 heads, so that the bias windows of a tile's heads stay small).
   f.pack = 1;
-  int64_t least = (int64_t)a.G * ((a.Sq + kTile - 1) / kTile);
+  int64_t least = a.G * (((int64_t)a.Sq + kTile - 1) / kTile);
   for (int g = 2; g <= 16 && g <= a.G; ++g) {
     const int tok = kTile / g;
-    const int64_t tiles = (int64_t)(a.G / g) * ((a.Sq + tok - 1) / tok);
+    const int64_t tiles = a.G / g * (((int64_t)a.Sq + tok - 1) / tok);
     if (a.G % g == 0 && tiles < least) {
       least = tiles;
       f.pack = g;
@@ -90,7 +90,7 @@ DenseFwdPlan dense_fwd_plan(const DenseDims& a) {
   }
   f.rep = a.Sq * f.pack <= kTile / 4 ? 4 : 1;
   f.tok = kTile / f.rep / f.pack;
-  f.ntile = (a.Sq + f.tok - 1) / f.tok;
+  f.ntile = (int)(((int64_t)a.Sq + f.tok - 1) / f.tok);
   f.dual = f.ntile == 1;
   const int npair = f.dual ? 1 : (f.ntile + 1) / 2;
   const int64_t blocks = (int64_t)a.B * (a.Hq / f.pack) * npair;
