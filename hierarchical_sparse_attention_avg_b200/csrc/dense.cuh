@@ -104,27 +104,36 @@ __device__ __forceinline__ uint32_t same_doc(int other, int mine) {
   return same;
 }
 
-// tanh, |error| <= about 2e-7 every way (the hardware's tanh has 5e-4: times a cap of 50 a score off by 0.02, more than
-// the operands' own rounding gives).  Where a warp's arguments are all small (scores below the cap, nearly always), an odd
-// polynomial on pairs, x p(x^2) with p fitted to tanh(x) / x for the least |error| of tanh (weighted least squares, the
-// weights raised where the error was large): on [0, 1/2] with 4 coefficients 1.6e-7, on [0, 5/4] with 8 coefficients 1.2e-7;
-// 6 or 10 packed FMAs a pair, against two exponentials and two reciprocals, whose pipe the softmax itself fills.
+// tanh with an error that goes by its own value (about 1e-6 of it), so that a score's does not go by the cap (the
+// hardware's tanh has 5e-4 absolute: times a cap of 50 a score off by 0.02, more than the operands' own rounding gives).
+// Small arguments take an odd polynomial x p(x^2), p fitted to tanh(x) / x for the least relative error (weighted least
+// squares, the weights raised where the error was large): 3 coefficients on [0, 1/4] 5.0e-7, 4 on [0, 1/2] 6.2e-7, 8 on
+// [0, 5/4] 1.8e-7, rounding included.  Beyond 1/4 the form by the exponential, some 1e-7 off, is as good; below it that
+// form's difference from 1 loses digits: 1e-2 of a score at a cap of 1e5, and 1.3e-5 at most up to a cap of 64, where the
+// forward does without the second form (Careful false; 617 against 827 us at 16 heads of 8,192 keys with many scores beyond
+// a cap of 20).  Where a warp's arguments are all small (scores below the cap, nearly always), the polynomials run on pairs:
+// 6 or 10 packed FMAs, against two exponentials and two reciprocals, whose pipe the softmax itself fills.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+constexpr float kCarefulCap = 64.f;
+template <bool Careful>
 __device__ __forceinline__ float tanh_any(float x) {
-  return fmaf(-2.f, rcp_approx(1.f + ex2(x * (2.f * 1.4426950408889634f))), 1.f);
+  const float far = fmaf(-2.f, rcp_approx(1.f + ex2(x * (2.f * 1.4426950408889634f))), 1.f);
+  if (!Careful) return far;
+  const float u = x * x, near = x * fmaf(fmaf(0.128416136f, u, -0.333219081f), u, 0.999999583f);
+  return fabsf(x) < 0.25f ? near : far;
 }
 template <bool Half>
 struct TanhPoly {  // f * tanh
   static constexpr int N = Half ? 4 : 8;
   uint64_t c[N];
   __device__ __forceinline__ explicit TanhPoly(float f) {
-    const float k4[4] = {0.999997677f, -0.33320657f, 0.131451624f, -0.0433729225f};
-    const float k8[8] = {0.999999512f, -0.333317329f, 0.133179241f, -0.0532919123f, 0.0202494413f, -0.00654016651f,
-                         0.00147954026f, -0.000164161214f};
+    const float k4[4] = {0.999999464f, -0.333263189f, 0.131902963f, -0.0444022231f};
+    const float k8[8] = {0.99999994f, -0.333326995f, 0.133245066f, -0.0534903407f, 0.0205571726f, -0.00679615559f,
+                         0.0015881143f, -0.000182598116f};
 #pragma unroll
     for (int i = 0; i < N; ++i) c[i] = f2pack((Half ? k4[i % 4] : k8[i]) * f, (Half ? k4[i % 4] : k8[i]) * f);
   }

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tanh32<false>(sv, cap_in, 1.f);
           } else {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) sv[c] = tanh_any(sv[c] * cap_in);
+            for (int c = 0; c < 32; ++c) sv[c] = tanh_any<true>(sv[c] * cap_in);
           }
         }
         uint32_t vis = 0xffffffffu;  // bit c: the pair (row0 + c, key) is visible

@@ -38,6 +38,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "dense.cuh"
 
@@ -77,7 +78,8 @@ struct FwdArgs {
   float *part_o, *part_lse;
 };
 
-template <int D, bool F16, bool CAP, int BIAS, int REP>
+// CAP: 0 none, 1 up to kCarefulCap, 2 beyond it; BIAS: 0 none, 1 slopes, 2 table; REP: copies of the queries.
+template <int D, bool F16, int CAP, int BIAS, int REP>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_fwd_kernel(const __grid_constant__ FwdMaps m, const __grid_constant__ FwdArgs p,
                      const __grid_constant__ BucketStarts starts) {
@@ -465,13 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           float mul = mul0;
           if (CAP) {
+            constexpr bool kPoly = REP == 1 || CAP == 2;  // (few rows are bound by memory: the short code serves them)
             float big = 0.f;
-            if constexpr (REP == 1) {  // (few rows are bound by memory: the short code serves them)
+            if constexpr (kPoly) {
 #pragma unroll
               for (int c = 0; c < CH; ++c) big = absmax32(s[c], big);
             }
             big *= cap_in;
-            if (REP == 1 && __all_sync(0xffffffffu, !valid || big <= 1.25f)) {
+            if (kPoly && __all_sync(0xffffffffu, !valid || big <= 1.25f)) {
 #pragma unroll
               for (int c = 0; c < CH; ++c) tanh32<false>(s[c], cap_in, mul0);
               mul = 1.f;
@@ -479,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[c][i] = tanh_any(s[c][i] * cap_in);
+                for (int i = 0; i < 32; ++i) s[c][i] = tanh_any<CAP == 2>(s[c][i] * cap_in);
             }
           }
           if (BIAS == 1) {
@@ -831,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool F16, bool CAP, int BIAS, int REP>
+template <int D, bool F16, int CAP, int BIAS, int REP>
 int launch_r(const FwdMaps& m, const FwdArgs& p, const BucketStarts& bs, int smem, cudaStream_t st) {
   auto kernel = dense_fwd_kernel<D, F16, CAP, BIAS, REP>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared-memory limit is set
@@ -847,7 +850,7 @@ int launch_r(const FwdMaps& m, const FwdArgs& p, const BucketStarts& bs, int sme
   kernel<<<grid, kThreads, smem, st>>>(m, p, bs);
   return check_launch();
 }
-template <int D, bool F16, bool CAP, int BIAS>
+template <int D, bool F16, int CAP, int BIAS>
 int launch_t(const FwdMaps& m, const FwdArgs& p, const BucketStarts& bs, int smem, cudaStream_t st) {
   return p.rep == 4 ? launch_r<D, F16, CAP, BIAS, 4>(m, p, bs, smem, st)
                     : launch_r<D, F16, CAP, BIAS, 1>(m, p, bs, smem, st);
@@ -856,13 +859,13 @@ int launch_t(const FwdMaps& m, const FwdArgs& p, const BucketStarts& bs, int sme
 template <int D, bool F16>
 int launch(const FwdMaps& m, const FwdArgs& p, const BucketStarts& bs, int smem, cudaStream_t st) {
   const int bias = p.a.slopes ? 1 : p.a.table ? 2 : 0;
-  const bool cap = p.a.cap > 0.f;
-  if (bias == 0) return cap ? launch_t<D, F16, true, 0>(m, p, bs, smem, st)
-                            : launch_t<D, F16, false, 0>(m, p, bs, smem, st);
-  if (bias == 1) return cap ? launch_t<D, F16, true, 1>(m, p, bs, smem, st)
-                            : launch_t<D, F16, false, 1>(m, p, bs, smem, st);
-  return cap ? launch_t<D, F16, true, 2>(m, p, bs, smem, st)
-             : launch_t<D, F16, false, 2>(m, p, bs, smem, st);
+  auto with = [&](auto tag) {
+    constexpr int C = decltype(tag)::value;
+    return bias == 0 ? launch_t<D, F16, C, 0>(m, p, bs, smem, st)
+                     : bias == 1 ? launch_t<D, F16, C, 1>(m, p, bs, smem, st) : launch_t<D, F16, C, 2>(m, p, bs, smem, st);
+  };
+  if (p.a.cap > kCarefulCap) return with(std::integral_constant<int, 2>{});
+  return p.a.cap > 0.f ? with(std::integral_constant<int, 1>{}) : with(std::integral_constant<int, 0>{});
 }
 
 }  // namespace fwd
