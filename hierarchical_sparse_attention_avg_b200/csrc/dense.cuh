@@ -13,6 +13,7 @@ namespace lh {
 constexpr int kMaxBuckets = 128;       // columns of the bias table
 constexpr int kMaxDenseKeys = 1 << 20; // keys per head (one flag byte per 128-key tile in shared memory)
 constexpr int kKeyTile = 128;
+constexpr float kMaxCapIn = 0x1p100f;  // (a score of zero times it is zero, any other one is at the cap)
 // Up to this many key tiles the forward's blocks take the ids' ranges of the tiles themselves (a few loads a warp);
 // beyond it they come from a launch of their own.
 constexpr int kOwnDocTiles = 32;
@@ -46,7 +47,7 @@ struct DenseDims {
   int f16;  // operands fp16 (else bf16)
   int causal;
   int buckets, near;  // table columns; distances of magnitude >= near share the end buckets
-  float scale, cap;
+  float scale, cap, cap_in;  // cap_in: scale / cap, at most kMaxCapIn
   const float* slopes;
   const void* table;
   const int32_t* docs;

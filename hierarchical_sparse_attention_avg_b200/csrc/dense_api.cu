@@ -8,6 +8,7 @@
 namespace lh {
 namespace {
 
+constexpr float kMinCap = 0x1p-80f, kMaxCap = 0x1p80f;
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 inline bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
@@ -71,7 +72,9 @@ int make_dense(const lh_attn_params* P, const lh_attn_mods* M, DenseDims* a, Buc
   a->f16 = P->dtype == LH_FP16;
   a->causal = P->causal;
   a->scale = P->scale;
-  a->cap = P->softcap;
+  // scale / cap and cap log2(e) stay normal numbers; scores near or beyond either bound do not tell them from the cap itself
+  a->cap = P->softcap > 0.f ? fminf(fmaxf(P->softcap, kMinCap), kMaxCap) : 0.f;
+  a->cap_in = a->cap > 0.f ? (float)fmin((double)P->scale / a->cap, (double)kMaxCapIn) : 0.f;
   if ((P->buckets > 0) != (M->table != nullptr) || (M->slopes && M->table)) return LH_ERR_INVALID_ARG;
   if (M->prefix && !P->causal) return LH_ERR_INVALID_ARG;
   if (!aligned4(M->slopes) || !aligned4(M->docs) || !aligned4(M->prefix) || !aligned4(M->kv_len) ||

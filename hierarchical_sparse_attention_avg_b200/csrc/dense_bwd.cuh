@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kid = doc_at(a, b, key, len);
     const bool kdead = kid < 0;
     const float mul = CAP ? a.cap * kLog2e : a.scale * kLog2e;
-    const float cap_in = a.scale / (CAP ? a.cap : 1.f);
+    const float cap_in = a.cap_in;
     const uint64_t mul2 = f2pack(mul, mul);
     const int E = a.near, wide = 2 * E + 1;
     float bacc[4] = {0.f, 0.f, 0.f, 0.f};  // lane l: dtable sums of buckets l, l + 32, ...

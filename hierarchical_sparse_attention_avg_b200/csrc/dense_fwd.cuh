@@ -392,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int jlast = valid ? last_key(a, x, len, prefix) : -1;
       const int mydoc = valid ? doc_at(a, b, x, len) : -1;
       const float mul0 = CAP ? a.cap * kLog2e : a.scale * kLog2e;
-      const float cap_in = a.scale / (CAP ? a.cap : 1.f);
+      // (a.cap_in as a constant operand of the loop is slower here: chunk 110 us against 103; the backward gains by it)
+      const float cap_in = CAP ? fminf(a.scale / a.cap, kMaxCapIn) : 0.f;
       const float slope2 = BIAS == 1 ? -__ldg(a.slopes + h) * kLog2e : 0.f;
       const int64_t trow = (int64_t)h * a.buckets;
       float* win = reinterpret_cast<float*>(smem + p.off_win) + q * p.win;

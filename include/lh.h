@@ -355,7 +355,7 @@ typedef struct lh_attn_params {
   int32_t dtype;                  /* LH_BF16 or LH_FP16: q, k, v, o, table and their gradients */
   int32_t causal;                 /* 0 or 1 */
   float scale;                    /* > 0 */
-  float softcap;                  /* >= 0; 0: none */
+  float softcap;                  /* >= 0; 0: none; taken as 2^-80 below that and as 2^80 beyond it */
   int32_t buckets;                /* columns of the table, 2 .. LH_MAX_BUCKETS (even and >= 4 if bidirectional); 0: none */
   int32_t max_distance;           /* > n / 2 with n the buckets of one direction (ignored without a table) */
   int32_t bidirectional;          /* 0 or 1 */

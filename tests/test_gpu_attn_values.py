@@ -61,3 +61,15 @@ def test_small_scores_beside_some_beyond_the_cap(lh, cuda_device, cap, Sq, d, dt
     assert raw[:, beyond].max() > cap and raw[:, ~beyond].max() < 100
     for n, g in _all(lh, P, q, k, v, dout, {}).items():
         A.check(n, g, ref)
+
+
+@pytest.mark.parametrize("cap", [1e-42, 1.2e-38, 1e-30, 1e24, 1e30, 2e38, 3.4e38])
+@pytest.mark.parametrize("Sq", [1, 130])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_caps_at_the_ends_of_the_type(lh, cuda_device, cap, Sq, dtype):
+    P = lh.AttnParams(1, 4, 2, Sq, 300, 64, dtype=dtype, softcap=cap)
+    x = A.make(P, 15, cuda_device, grad=True)
+    x[0][:, 0] = 0.0  # scores of nothing too
+    ref = A.reference(P, *x[:3], dout=x[3])
+    for n, g in _all(lh, P, *x, {}).items():
+        A.check(n, g, ref)
