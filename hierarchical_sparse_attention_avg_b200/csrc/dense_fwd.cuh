@@ -58,6 +58,12 @@ constexpr uint32_t kSmemLimit = 226 * 1024;  // dynamic shared memory of a block
 // signs, with slopes), 6 a value row that is not finite was cleared
 constexpr int kSees = 1, kMasked = 4, kNear = 16, kBad = 64;
 
+// An exponent is one FMA, score * mul + (shift - maximum), with the second term rounded to a step of the maximum.  Beyond
+// this magnitude (of log2) the largest probability would be more than 2^(1/16) off 1, overflow fp16 from 2^25 on, and
+// vanish or overflow fp32 from 2^31 on: there the score is rounded before the maximum is taken off.  (The test for it costs
+// 1 %, with slopes 2 %: 16,384 rows 569 -> 582 us; a cap of at most 64 without a bias does without.)
+constexpr float kFarMax = 1048576.f;
+
 // Registers a thread: 128 * 56 + 256 * 224 = 384 * 168, what the block is launched with.
 constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
 
@@ -398,6 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t trow = (int64_t)h * a.buckets;
       float* win = reinterpret_cast<float*>(smem + p.off_win) + q * p.win;
       float m_run = -INFINITY, l_run = 0.f;
+      constexpr bool kMayBeFar = CAP != 1 || BIAS != 0;  // (no score is beyond kCarefulCap else)
+      bool far = false;                                  // some row's maximum is beyond kFarMax
       bool ok = true;
       int cnt = 0;
       const int ring = p.dual ? q * p.slots : 0, mask = p.dual ? 1 << q : 3;
@@ -560,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             alpha = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
             l_run *= alpha;
             m_run = m_new;
+            if (kMayBeFar) far = __any_sync(0xffffffffu, valid && m_run != -INFINITY && fabsf(m_run) > kFarMax);
           }
           // O_q's last product has completed (it was issued before these scores): bring O_q to the new maximum
           if (cnt > 0 && move) {
@@ -574,7 +583,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           // P over the first 64 columns of S, and its row sum; a row that has seen no key yet keeps P = 0
-          const float sub = cadd + kShift - (m_run == -INFINITY ? 0.f : m_run);
+          float sub = cadd + kShift - (m_run == -INFINITY ? 0.f : m_run);
+          if (kMayBeFar && __builtin_expect(far, 0)) {  // the score rounded first, then the difference, exact near the maximum
+            const float top = m_run == -INFINITY ? 0.f : m_run;
+            const uint64_t mul2 = f2pack(mul, mul), cadd2 = f2pack(cadd, cadd), top2 = f2pack(-top, -top);
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const uint64_t z = add_f32x2(fma_f32x2(f2pack(s[c][i], s[c][i + 1]), mul2, cadd2), top2);
+                s[c][i] = f2lo(z);
+                s[c][i + 1] = f2hi(z);
+              }
+            mul = 1.f;
+            sub = kShift;
+          }
           uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
           const uint64_t mul2 = f2pack(mul, mul), sub2 = f2pack(sub, sub), one2 = f2pack(1.f, 1.f);
           auto pair = [&](int c, int i) {  // the probabilities of columns i, i + 1 of run c, packed

@@ -73,3 +73,40 @@ def test_caps_at_the_ends_of_the_type(lh, cuda_device, cap, Sq, dtype):
     ref = A.reference(P, *x[:3], dout=x[3])
     for n, g in _all(lh, P, *x, {}).items():
         A.check(n, g, ref)
+
+
+def _peaks(P, dev, size, tie):
+    """Rows whose scores are whole multiples of `size` (exact in fp32), one key (or `tie` of them) the largest."""
+    g = torch.Generator().manual_seed(16)
+    q, k, v, dout = A.make(P, 16, dev, grad=True)
+    q.zero_(), k.zero_()
+    q[..., 0] = 2.0 ** math.ceil(math.log2(size) / 2)
+    step = size / float(q.flatten()[0])
+    order = torch.stack([torch.randperm(P.Skv, generator=g) for _ in range(P.B * P.Hkv)]).view(P.B, P.Hkv, P.Skv)
+    level = torch.where(order < tie, torch.full_like(order, 3), order % 3).to(dev)  # 3 for the winners, 0 .. 2 elsewhere
+    k[..., 0] = (step * level).to(P.dtype)
+    win = (level == 3)[:, :, None, :].repeat_interleave(P.Hq // P.Hkv, 1).double()  # [B, Hq, 1, Skv]
+    return q, k, v, dout, win / win.sum(3, keepdim=True), 3.0 * size
+
+
+@pytest.mark.parametrize("dtype,size", [(BF, 2.0 ** e) for e in (10, 20, 24, 27, 30, 36, 60)] +
+                         [(FP, 2.0 ** e) for e in (10, 20, 24, 26, 27)])
+@pytest.mark.parametrize("tie", [1, 2])
+@pytest.mark.parametrize("Sq,Skv,d,bias", [
+    (1, 500, 64, ""), (1, 9000, 128, ""), (9, 500, 128, ""), (60, 700, 64, ""), (300, 700, 64, ""), (520, 520, 128, ""),
+    (300, 300, 64, "slopes"), (300, 300, 128, "table"), (1, 500, 128, "table"),
+])
+def test_large_scores_are_a_choice_of_keys(lh, cuda_device, size, tie, dtype, Sq, Skv, d, bias):
+    """Finite scores of any size: nothing overflows, and the softmax is the choice of the largest key (or of two)."""
+    if bias and tie > 1:
+        pytest.skip("a bias parts equal scores")
+    f = dict(buckets=32, max_distance=128) if bias == "table" else {}
+    P = lh.AttnParams(1, 4, 2, Sq, Skv, d, dtype=dtype, causal=False, scale=1.0, **f)
+    q, k, v, dout, p, top = _peaks(P, cuda_device, size, tie)
+    m = mods(P, cuda_device, slopes=bias == "slopes")  # (biases of at most 75: far below the steps)
+    o, lse = lh.lh_attn_forward(P, q, k, v, **m)
+    V, u = v.double().repeat_interleave(2, 1), A.half_step(P)
+    want, mean = ((p @ x).expand(1, 4, Sq, d) for x in (V, V.abs()))
+    assert torch.isfinite(o).all() and ((o.double() - want).abs() <= (2 * u + 2.0 ** -14) * mean + 1e-7).all()
+    # lse: four roundings of numbers up to log2(e) times the top score, the bias or the logarithm of the tie
+    assert ((lse.double() - top).abs() <= 8 * 2.0 ** -24 * top + (75.0 if bias else math.log(tie) + 1e-3)).all()
