@@ -165,6 +165,12 @@ __device__ __forceinline__ void tanh32(float (&v)[32], float in, float f) {
     }
   }
 }
+// The smaller one; NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // Largest magnitude of 32 values against m.
 __device__ __forceinline__ float absmax32(const float (&v)[32], float m) {
   float a = m, b = 0.f, c = 0.f, d = 0.f;

@@ -42,6 +42,9 @@ constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kBarCompute = 1, kBarDrain = 2;
 constexpr int kHeadFastBelow = 148;
+// LSE is rounded to a step of its size, and so is each term of the exponent: from this magnitude (of log2) on a P of 1 could
+// come out as more than 2^(3/16), and at scores of 2^25 as 2^8.
+constexpr float kFarTerm = 1048576.f;
 constexpr float kShift16 = 4096.f;  // fp16: P is carried times this
 
 template <int D>
@@ -291,7 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool near = false;
         float badd = 0.f;
         int bucket = 0;
-        if (BIAS == 1) near = x0 - (kw + 31) < 0;
+        const int d0 = x0 - key;  // distance of column 0
+        if (BIAS == 1) {
+          near = x0 - (kw + 31) < 0;
+          // a tile on one side of the slopes: the statistics hold the columns' share, this is the key's and the tile's
+          if (!near) badd = slope2 * (float)(d0 - 32 * hc);
+        }
         if (BIAS == 2) {
           const int lo = min(max(x0 - (kw + 31), -E), E), hi = min(max(x0 + 31 - kw, -E), E);
           bucket = __ldg(p.w.bucket + E + hi);
@@ -305,6 +313,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_ld32(tmem + 128 * i + lane_base + 32 * hc, sv);
         tmem_ld32(tmem + 128 * i + 64 + lane_base + 32 * hc, dp);
+        bool far = false;
+        if (BIAS == 1) {
+          const float nlse = reinterpret_cast<const float*>(smem + Lay::STAT + s * Lay::ST)[32 * hc + lane];
+          far = __any_sync(0xffffffffu, (fabsf(nlse) > kFarTerm && nlse != -INFINITY) || fabsf(badd) > kFarTerm);
+        }
         tmem_ld_wait();
         if (CAP) {
           const float big = absmax32(sv, 0.f) * cap_in;
@@ -326,12 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pk[16], dk[16];
         const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * Lay::ST) + 8 * hc;
         const ulonglong2* nd4 = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * Lay::ST + kQTile * 4) + 8 * hc;
-        const int d0 = x0 - key;  // distance of column 0
-        // a tile on one side of the slopes: the statistics hold the columns' share, this is the key's and the tile's
-        if (BIAS == 1 && !near) badd = slope2 * (float)(d0 - 32 * hc);
         const uint64_t badd2 = f2pack(badd, badd);
         uint64_t sum2 = 0ull;
-        // P and dS of the 32 columns; Near: the bias differs from pair to pair
+        // P and dS of the 32 columns; Near: the bias differs from pair to pair.  P is kept at 1 at most; with slopes only
+        // where the exponent's terms are large, in the form for any pair (16,384 rows, backward 1420 us; kept there for every
+        // pair too 1487; the other kernels pay up to 1 % for it, and up to 13 % for a second form of the loop)
+        constexpr float top = F16 ? 12.f : 0.f;
         auto columns = [&](auto tag) {
           constexpr bool Near = decltype(tag)::value;
 #pragma unroll
@@ -342,13 +355,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int cc = c + 2 * h;
               uint64_t arg = fma_f32x2(f2pack(sv[cc], sv[cc + 1]), mul2, h ? nl.y : nl.x);
               if (BIAS != 0 && !Near) arg = add_f32x2(arg, badd2);
-              if (BIAS == 1 && Near) {
+              if (BIAS == 1 && Near) {  // (also right on one side)
                 auto bb = [&](int e) { return slope2 * (fabsf((float)(d0 + e)) - (float)(32 * hc + e)); };
                 arg = add_f32x2(arg, f2pack(bb(cc), bb(cc + 1)));
               }
               if (BIAS == 2 && Near)
                 arg = add_f32x2(arg, f2pack(__ldg(bias + min(max(d0 + cc, -E), E)), __ldg(bias + min(max(d0 + cc + 1, -E), E))));
-              const float p0 = ex2(f2lo(arg)), p1 = ex2(f2hi(arg));
+              float a0 = f2lo(arg), a1 = f2hi(arg);
+              if (Near || BIAS != 1) a0 = min_nan(a0, top), a1 = min_nan(a1, top);
+              const float p0 = ex2(a0), p1 = ex2(a1);
               uint64_t z2 = mul_f32x2(f2pack(p0, p1), add_f32x2(f2pack(dp[cc], dp[cc + 1]), h ? nd.y : nd.x));
               pk[cc / 2] = pack2_rn<F16>(p0, p1);
               if (BIAS == 2) {
@@ -365,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        if (BIAS != 0 && near) columns(std::true_type{});
+        if (BIAS != 0 && (near || far)) columns(std::true_type{});
         else columns(std::false_type{});
         if (!whole) {  // masked pairs are nothing, whatever came out
           sum2 = 0ull;

@@ -397,7 +397,8 @@ int lh_attn_forward(const lh_attn_params* P, const lh_attn_mods* M, const lh_ten
  * its query heads) and, with a table, dtable [Hq, buckets].  q, k, v, M as in the forward; o and lse its results.  low:
  * NULL, or the forward's: dZ = P (dP - <dout, o>) takes a small difference, so o's own rounding is the largest error of
  * the gradients without it (bf16: dq, dk 2.4e-3 off the formula in the 2-norm with it, 4.2e-3 without, dtable up to
- * 7e-3).  A bucket's dtable may also be off by 2^-20 of the |dZ| summed over the buckets next to it.  dk, dv and dtable
+ * 7e-3).  The probabilities are exp(z - lse), at most 1, so the rounding of lse is a factor of up to 1 + |lse| 2^-22 in every
+ * gradient: 2e-4 at |lse| = 1000, and beyond 10^6 their size is no longer held.  A bucket's dtable may also be off by 2^-20 of the |dZ| summed over the buckets next to it.  dk, dv and dtable
  * are bitwise reproducible; dq is accumulated with fp32 reduce-adds in no fixed order before it is rounded. */
 int lh_attn_backward(const lh_attn_params* P, const lh_attn_mods* M, const lh_tensor* q, const lh_tensor* k,
                      const lh_tensor* v, const lh_tensor* o, const lh_tensor* low, const float* lse,

@@ -110,3 +110,39 @@ def test_large_scores_are_a_choice_of_keys(lh, cuda_device, size, tie, dtype, Sq
     assert torch.isfinite(o).all() and ((o.double() - want).abs() <= (2 * u + 2.0 ** -14) * mean + 1e-7).all()
     # lse: four roundings of numbers up to log2(e) times the top score, the bias or the logarithm of the tie
     assert ((lse.double() - top).abs() <= 8 * 2.0 ** -24 * top + (75.0 if bias else math.log(tie) + 1e-3)).all()
+
+
+@pytest.mark.parametrize("dtype,size", [(BF, 2.0 ** e) for e in (10, 20, 24, 27, 30, 36, 60)] +
+                         [(FP, 2.0 ** e) for e in (10, 20, 24, 26, 27)])
+@pytest.mark.parametrize("tie", [1, 2])
+@pytest.mark.parametrize("Sq,Skv,d,bias", [
+    (1, 500, 64, ""), (1, 9000, 128, ""), (9, 500, 128, ""), (60, 700, 64, ""), (300, 700, 64, ""), (520, 520, 128, ""),
+    (300, 300, 64, "slopes"), (300, 300, 128, "table"), (1, 500, 128, "table"),
+])
+def test_gradients_of_large_scores(lh, cuda_device, size, tie, dtype, Sq, Skv, d, bias):
+    """The same scores: finite gradients, of probabilities that are at most 1."""
+    if bias and tie > 1:
+        pytest.skip("a bias parts equal scores")
+    f = dict(buckets=32, max_distance=128) if bias == "table" else {}
+    P = lh.AttnParams(1, 4, 2, Sq, Skv, d, dtype=dtype, causal=False, scale=1.0, **f)
+    q, k, v, dout, p, top = _peaks(P, cuda_device, size, tie)
+    m, u = mods(P, cuda_device, slopes=bias == "slopes"), A.half_step(P)
+    o, lse = lh.lh_attn_forward(P, q, k, v, **m)
+    grads = lh.lh_attn_backward(P, q, k, v, o, lse, dout, **m)
+    # what P <= 1 allows: |dZ| = |dP - D| at the keys chosen, with D of a rounded o; beyond the type's largest number
+    # a gradient is infinite, and nowhere is it NaN
+    heads = lambda a: a.view(1, 2, 2, Skv, d).sum(2)  # noqa: E731
+    V, W, win = v.double().repeat_interleave(2, 1), dout.double(), (p > 0).expand(1, 4, Sq, Skv)
+    dP = W @ V.transpose(2, 3)
+    Z = ((dP - (dP * p).sum(3, keepdim=True)).abs() + 4 * u * (W.abs() @ V.abs().transpose(2, 3))) * win
+    most = (Z @ k.double().abs().repeat_interleave(2, 1), heads(Z.transpose(2, 3) @ q.double().abs()),
+            heads(win.double().transpose(2, 3) @ W.abs()), torch.zeros(()))
+    for g, b in zip(grads, most):
+        if g is not None:
+            assert not torch.isnan(g).any() and (torch.isfinite(g) | (b > 0.9 * torch.finfo(dtype).max).to(g.device)).all()
+    if not bias:
+        # P = exp(z - lse) is a factor exp(error of lse) off, of at most 1: dv by as much of its own sum
+        mass = lambda a: (p.expand(1, 4, Sq, Skv).transpose(2, 3) @ a).view(1, 2, 2, Skv, d).sum(2)  # noqa: E731
+        off = math.expm1(min(12 * 2.0 ** -24 * top, 0.5)) if size < 2.0 ** 19 else 1.0
+        got, W = grads[2].double(), mass(dout.double())
+        assert ((got - W).abs() <= (off + 2 * u + 2.0 ** -14) * mass(dout.double().abs()) + 1e-6).all()
