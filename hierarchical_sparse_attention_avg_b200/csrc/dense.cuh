@@ -228,6 +228,15 @@ template <bool F16>
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return F16 ? (((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u) : (((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u);
 }
+// The larger magnitude of each of two 16-bit values (signs as they come), NaN if either is: nonfinite2 of it tells whether one
+// of them is not finite, at one instruction a word.
+template <bool F16>
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (F16) asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // 8 features as 16-bit values, and what the rounding dropped.
 template <bool F16>

@@ -441,17 +441,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBSF + q), cnt & 1, &s_wait, status));
         if (!ok) continue;  // (the group's later barriers still count this warp)
         tc_fence_after();
-        if (masked) {  // value rows that may meet a probability of zero: clear what is not finite (thread = row)
+        // Value rows that may meet a probability of zero: clear what is not finite (thread = row).  Both tiles of a block do so
+        // where one has masked pairs, each ahead of its own product: V is theirs together, and whether the other's clearing
+        // comes first must not show.
+        if (f & (3 * kMasked)) {
           ok = __all_sync(0xffffffffu, mbar_wait(bar(kBFull + ring + r.s), r.ph, &s_wait, status));
           if (!ok) continue;  // (the group's later barriers still count this warp)
           uint8_t* vr = smem + p.off_kv + (ring + r.s) * TILE + row * 128;
           uint32_t bad = 0;
           if (!dead) {
+            uint4 most = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
               const uint4 w = *reinterpret_cast<const uint4*>(vr + (i >> 3) * 16384 + (((i + lane) & 7) << 4));
-              bad |= nonfinite2<F16>(w.x) | nonfinite2<F16>(w.y) | nonfinite2<F16>(w.z) | nonfinite2<F16>(w.w);
+              most.x = absmax2<F16>(most.x, w.x);
+              most.y = absmax2<F16>(most.y, w.y);
+              most.z = absmax2<F16>(most.z, w.z);
+              most.w = absmax2<F16>(most.w, w.w);
             }
+            bad = nonfinite2<F16>(absmax2<F16>(absmax2<F16>(most.x, most.y), absmax2<F16>(most.z, most.w)));
           }
           if (dead) {
 #pragma unroll

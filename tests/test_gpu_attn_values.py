@@ -146,3 +146,44 @@ def test_gradients_of_large_scores(lh, cuda_device, size, tie, dtype, Sq, Skv, d
         off = math.expm1(min(12 * 2.0 ** -24 * top, 0.5)) if size < 2.0 ** 19 else 1.0
         got, W = grads[2].double(), mass(dout.double())
         assert ((got - W).abs() <= (off + 2 * u + 2.0 ** -14) * mass(dout.double().abs()) + 1e-6).all()
+
+
+@pytest.mark.parametrize("junk", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, FP)])
+def test_values_that_are_not_finite_under_vanished_probabilities(lh, cuda_device, junk, d, dtype):
+    """A key so low that every row's probability of it is nothing, its value not finite: the rows of both query tiles of a
+    block that share it come out one way, call after call."""
+    P = lh.AttnParams(1, 8, 4, 512, 512, d, dtype=dtype)
+    q, k, v = A.make(P, 17, cuda_device)
+    q[..., 0], k[..., 0] = 64.0, 0.0
+    at = [10, 70, 127, 300]
+    k[:, :, at, 0] = -64.0  # scores lower by 360 and more
+    v[:, :, at, 5] = junk
+    first = lh.lh_attn_forward(P, q, k, v)
+    for i in range(60):
+        o, lse = lh.lh_attn_forward(P, q, k, v)
+        assert torch.equal(lse, first[1])
+        assert torch.equal(o.view(torch.int16), first[0].view(torch.int16)), i
+    sees = torch.arange(512, device=cuda_device) >= 10
+    assert not torch.isfinite(o[:, :, sees, 5]).any() and torch.isfinite(o[:, :, ~sees]).all()
+    keep = torch.arange(d, device=cuda_device) != 5
+    ref = A.reference(P, q, k, v.nan_to_num(0.0, 0.0, 0.0))
+    A.check("o", o[..., keep], {n: ref[n][..., keep] for n in ("o", "e_o")})
+
+
+@pytest.mark.parametrize("junk", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("d,dtype", [(64, BF), (64, FP), (128, BF), (128, FP)])
+def test_both_query_tiles_take_a_value_that_is_not_finite_the_same_way(lh, cuda_device, junk, d, dtype):
+    """The first query tile sees a key tile whole, the second one part of it (documents): a value that is not finite, under
+    a probability of nothing, is what comes out of either."""
+    P = lh.AttnParams(1, 2, 2, 256, 256, d, dtype=dtype, causal=False)
+    q, k, v = A.make(P, 18, cuda_device)
+    m = mods(P, cuda_device, docs=[spans(256, 192, 64)])
+    q[..., 0], k[..., 0] = 64.0, 0.0
+    k[:, :, 20, 0] = -64.0
+    v[:, :, 20, d - 1] = junk
+    for _ in range(20):
+        o, _ = lh.lh_attn_forward(P, q, k, v, **m)
+        hit = o[:, :, :192, d - 1].float()
+        assert (torch.isnan(hit) if junk != junk else hit == junk).all()
+        assert torch.isfinite(o[:, :, 192:]).all() and torch.isfinite(o[..., :d - 1]).all()
