@@ -328,7 +328,7 @@ struct DenseFwdPlan {
   int nsplit;  // blocks that share one query tile's keys
 };
 DenseFwdPlan dense_fwd_plan(const DenseDims& a);
-// dense_prep.cu: ids' range (min, max) of every key tile: kdoc [B][ceil(Skv / 128)].
+// dense_prep.cu: ids' range (as id_range has it) of every key tile: kdoc [B][ceil(Skv / 128)].
 int launch_dense_doc_ranges(const DenseDims& a, int2* kdoc, cudaStream_t st);
 // dense_fwd.cu: low.p may be null; part_o / part_lse: nsplit > 1 only.
 int launch_dense_fwd(const DenseDims& a, const BucketStarts& bs, const DenseTensor& q, const DenseTensor& k,

@@ -77,7 +77,9 @@ using namespace fwd;
 DenseFwdPlan dense_fwd_plan(const DenseDims& a) {
   DenseFwdPlan f;
   // The query heads of a key head share query tiles where that takes fewer of them than tiles of one head each (few
-  // tokens; at most 16 heads, so that the bias windows of a tile's heads stay small).
+  // tokens): a divisor of the group, so that a tile belongs to one key head, of at most 16, so that the bias windows of a
+  // tile's heads leave the ring its place (one rule with and without a table).  A group whose divisors are larger, as 17,
+  // reads its keys once for each head.
   f.pack = 1;
   int64_t least = a.G * (((int64_t)a.Sq + kTile - 1) / kTile);
   for (int g = 2; g <= 16 && g <= a.G; ++g) {
@@ -96,8 +98,8 @@ DenseFwdPlan dense_fwd_plan(const DenseDims& a) {
   const int64_t blocks = (int64_t)a.B * (a.Hq / f.pack) * npair;
   const int nk = (a.Skv + kTile - 1) / kTile;
   // Fewer blocks than SMs: the shares of the keys that are through first, counted in key tiles: rounds of blocks times a
-  // block's tiles and about four for its start and end, and two for the join (120 blocks in one round against 280 in two,
-  // 9 x 128-row tiles over 128 key tiles: 134 us against 127).
+  // block's tiles and about four for its start and end, and two for the join (5 pairs of 128-row tiles over 128 key tiles,
+  // 8 head groups: 107 us in one round of 120 blocks, 103 in two of 280).
   f.nsplit = 1;
   int64_t best = nk + 4;
   for (int rounds = 1; blocks < kSms && rounds <= 2; ++rounds) {

@@ -26,12 +26,13 @@
 // reads the bias from a window of distances in shared memory; slopes are one FMA more.
 //
 // Masked places: a masked score is overwritten after it is computed, whatever it was.  A value row that is not finite
-// would still reach other rows through 0 * inf, so in tiles with masked pairs the softmax threads clear such rows of V
-// in shared memory before the product (dead rows for good; others are added to the rows that see them at the end).
+// would still reach other rows through 0 * inf, so in key tiles with masked pairs for either query tile of the block the
+// softmax threads of both clear such rows of V in shared memory before their product (dead rows for good; others are added
+// to the rows that see them at the end).
 //
 // Precision: Q, K, V enter as they are, scores and statistics fp32; the probabilities are rounded once to the operands'
-// type (2^-9 bf16, 2^-12 fp16 relative), as both operands of one tensor-core product must share it.  They are taken against
-// the running maximum itself, so that a row's largest one is 1 and exact: with a maximum that only moves when exceeded by
+// type (by at most 2^-8 bf16, 2^-11 fp16 relative), as both operands of one tensor-core product must share it.  They are taken
+// against the running maximum itself, so that a row's largest one is 1 up to fp32 rounding: with a maximum that only moves when exceeded by
 // 2^8 the accumulator is rescaled more rarely (269 us instead of 275 at 16 heads of 8,192 causal keys), but <dO, O>, which
 // the backward subtracts from nearly equal numbers, then makes bf16 dQ and dK 2.8e-3 off instead of 2.4e-3.
 // fp16 probabilities are carried times 2^14, so that the many small ones of a long row beside one large key do not vanish.

@@ -7,8 +7,8 @@ namespace lh {
 
 namespace {
 
-// The ids' range (min, max; a dead position counts as -1) of tile w: key tiles first, then 64-row query sub-tiles.  One
-// warp each.
+// The ids' range of tile w (its live positions' least and largest id, the least one complemented where a position is dead:
+// id_range): key tiles first, then 64-row query sub-tiles.  One warp each.
 __device__ __forceinline__ void doc_range(const DenseDims& a, int b, int w, int lane, int nk, int2* kdoc, int2* qdoc,
                                           int nq) {
   const int len = dense_len(a, b);

@@ -344,8 +344,8 @@ int lh_cp_backward_unpool(const lh_params* P, int G, int rank, const void* ctx, 
  * A position with a negative id, a key at or beyond kv_len and a row with x < 0 take part in nothing: whatever their
  * rows of q, k, v and dout hold (NaN included) reaches no other row.  In the forward the same holds for every masked
  * pair, and a visible value that is not finite leaves its feature of the rows that see it not finite (an infinity or NaN,
- * whatever its probability, the same in every call); in the backward a value that is not finite at a visible position may also reach gradients of rows and keys of
- * its 128-key and 64-row tiles.
+ * whatever its probability, the same in every call); in the backward a value that is not finite at a visible position may
+ * also reach gradients of rows and keys of its 128-key and 64-row tiles.
  * Supported: d in {64, 128}, bf16 or fp16, Hkv | Hq, B Hq <= 65535, Skv <= 2^20, B Hq Sq < 2^31. */
 #define LH_BF16 0
 #define LH_FP16 1

@@ -89,17 +89,17 @@ def _peaks(P, dev, size, tie):
     return q, k, v, dout, win / win.sum(3, keepdim=True), 3.0 * size
 
 
+# (a bias parts equal scores: ties without one only)
+PEAKS = [(Sq, Skv, d, "", tie) for Sq, Skv, d in ((1, 500, 64), (1, 9000, 128), (9, 500, 128), (60, 700, 64), (300, 700, 64),
+                                                  (520, 520, 128)) for tie in (1, 2)]
+PEAKS += [(300, 300, 64, "slopes", 1), (300, 300, 128, "table", 1), (1, 500, 128, "table", 1)]
+
+
 @pytest.mark.parametrize("dtype,size", [(BF, 2.0 ** e) for e in (10, 20, 24, 27, 30, 36, 60)] +
                          [(FP, 2.0 ** e) for e in (10, 20, 24, 26, 27)])
-@pytest.mark.parametrize("tie", [1, 2])
-@pytest.mark.parametrize("Sq,Skv,d,bias", [
-    (1, 500, 64, ""), (1, 9000, 128, ""), (9, 500, 128, ""), (60, 700, 64, ""), (300, 700, 64, ""), (520, 520, 128, ""),
-    (300, 300, 64, "slopes"), (300, 300, 128, "table"), (1, 500, 128, "table"),
-])
-def test_large_scores_are_a_choice_of_keys(lh, cuda_device, size, tie, dtype, Sq, Skv, d, bias):
+@pytest.mark.parametrize("Sq,Skv,d,bias,tie", PEAKS)
+def test_large_scores_are_a_choice_of_keys(lh, cuda_device, size, dtype, Sq, Skv, d, bias, tie):
     """Finite scores of any size: nothing overflows, and the softmax is the choice of the largest key (or of two)."""
-    if bias and tie > 1:
-        pytest.skip("a bias parts equal scores")
     f = dict(buckets=32, max_distance=128) if bias == "table" else {}
     P = lh.AttnParams(1, 4, 2, Sq, Skv, d, dtype=dtype, causal=False, scale=1.0, **f)
     q, k, v, dout, p, top = _peaks(P, cuda_device, size, tie)
@@ -114,15 +114,9 @@ def test_large_scores_are_a_choice_of_keys(lh, cuda_device, size, tie, dtype, Sq
 
 @pytest.mark.parametrize("dtype,size", [(BF, 2.0 ** e) for e in (10, 20, 24, 27, 30, 36, 60)] +
                          [(FP, 2.0 ** e) for e in (10, 20, 24, 26, 27)])
-@pytest.mark.parametrize("tie", [1, 2])
-@pytest.mark.parametrize("Sq,Skv,d,bias", [
-    (1, 500, 64, ""), (1, 9000, 128, ""), (9, 500, 128, ""), (60, 700, 64, ""), (300, 700, 64, ""), (520, 520, 128, ""),
-    (300, 300, 64, "slopes"), (300, 300, 128, "table"), (1, 500, 128, "table"),
-])
-def test_gradients_of_large_scores(lh, cuda_device, size, tie, dtype, Sq, Skv, d, bias):
+@pytest.mark.parametrize("Sq,Skv,d,bias,tie", PEAKS)
+def test_gradients_of_large_scores(lh, cuda_device, size, dtype, Sq, Skv, d, bias, tie):
     """The same scores: finite gradients, of probabilities that are at most 1."""
-    if bias and tie > 1:
-        pytest.skip("a bias parts equal scores")
     f = dict(buckets=32, max_distance=128) if bias == "table" else {}
     P = lh.AttnParams(1, 4, 2, Sq, Skv, d, dtype=dtype, causal=False, scale=1.0, **f)
     q, k, v, dout, p, top = _peaks(P, cuda_device, size, tie)
